@@ -40,6 +40,9 @@ __all__ = [
     "spec_verify_status_string", "spec_verify_version", "spec_verify_pool_allocations", "verify", "sample",
     "spec_verify_tree", "spec_verify_tree_ex", "spec_verify_tree_workspace_size", "verify_tree",
     "spec_verify_head_greedy", "spec_verify_head_workspace_size", "verify_head_greedy",
+    "KvCache", "SvCache", "SV_DTYPE_F16", "cache_lib", "cache_attend", "cache_append", "cache_read",
+    "spec_cache_attend", "spec_cache_append", "spec_cache_read", "spec_cache_attend_workspace_size",
+    "spec_cache_page_bytes",
 ]
 
 
@@ -463,3 +466,8 @@ def sample(logits, uniforms=None, temperature=None, top_k: int = 0, greedy: bool
     if st != SV_OK:
         raise SpecVerifyError(st, "spec_sample_ex")
     return out_tokens
+
+
+from .cache import (  # noqa: E402  (the 4-bit key/value cache; it uses the helpers above)
+    SV_DTYPE_F16, KvCache, SvCache, cache_append, cache_attend, cache_lib, cache_read, spec_cache_append,
+    spec_cache_attend, spec_cache_attend_workspace_size, spec_cache_page_bytes, spec_cache_read)

@@ -1,4 +1,4 @@
-"""Build ``libspec_verify.so`` (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Build ``libspec_verify.so`` and ``libspec_cache.so`` (the C-ABI libraries) in-tree with nvcc for sm_100a."""
 from __future__ import annotations
 
 import os
@@ -8,9 +8,20 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libspec_verify.so")
-SOURCES = [os.path.join(CSRC, "spec_verify.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("sv_common.cuh", "sv_rows.cuh", "sv_seq.cuh", "sv_resid.cuh", "sv_ptx.cuh", "sv_procs.cuh", "sv_nucleus.cuh", "sv_tree.cuh", "sv_head.cuh")] + [
-    os.path.join(ROOT, "include", "spec_verify.h")]
+CACHE_LIB = os.path.join(HERE, "libspec_cache.so")
+HEADER = os.path.join(ROOT, "include", "spec_verify.h")
+
+
+def _csrc(*names):
+    return [os.path.join(CSRC, f) for f in names]
+
+
+SOURCES = _csrc("spec_verify.cu")
+DEPS = SOURCES + _csrc("sv_common.cuh", "sv_rows.cuh", "sv_seq.cuh", "sv_resid.cuh", "sv_ptx.cuh", "sv_procs.cuh",
+                       "sv_nucleus.cuh", "sv_tree.cuh", "sv_head.cuh") + [HEADER]
+CACHE_SOURCES = _csrc("spec_cache.cu")
+CACHE_DEPS = CACHE_SOURCES + _csrc("sc_common.cuh", "sc_attend.cuh", "sc_store.cuh", "sv_ptx.cuh") + [
+    HEADER, os.path.join(ROOT, "include", "spec_cache.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -26,19 +37,21 @@ def nvcc() -> str:
     return path if os.path.exists(path) else "nvcc"
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def up_to_date(lib: str = LIB, deps=None) -> bool:
+    if not os.path.exists(lib):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in DEPS)
+    t = os.path.getmtime(lib)
+    return all(os.path.getmtime(p) <= t for p in (DEPS if deps is None else deps))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-o", LIB + ".tmp"] + SOURCES
-    subprocess.run(cmd, check=True)
-    os.replace(LIB + ".tmp", LIB)
+    """Build what is out of date; returns the path of ``libspec_verify.so``."""
+    for lib, sources, deps in ((LIB, SOURCES, DEPS), (CACHE_LIB, CACHE_SOURCES, CACHE_DEPS)):
+        if not force and up_to_date(lib, deps):
+            continue
+        cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-o", lib + ".tmp"] + sources
+        subprocess.run(cmd, check=True)
+        os.replace(lib + ".tmp", lib)
     return LIB
 
 

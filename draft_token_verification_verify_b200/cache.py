@@ -1,0 +1,360 @@
+"""The 4-bit key/value cache beside verification: Python binding of ``spec_cache.h``.
+
+Argument marshalling only, over ``libspec_cache.so``; there is no Python or
+CPU fallback.  ``cache_attend`` scores the k+1 positions of every sequence
+against the cached context and themselves, ``cache_append`` keeps the accepted
+positions (as ``verify`` and ``verify_tree`` report them), ``cache_read`` reads
+a range back.  Tensors are checked for dtype, shape, strides and device before
+the call (TypeError / ValueError).
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+import os
+from typing import Optional
+
+from . import _build
+
+SV_DTYPE_F16 = 2 << 8
+
+CACHE_LIB_PATH = _build.CACHE_LIB
+
+
+class SvCache(ctypes.Structure):
+    """Mirror of ``sv_cache_t``."""
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+    ]
+
+
+_cache_lib = None
+
+
+def cache_lib() -> ctypes.CDLL:
+    """Load the cache's C-ABI library (built in-tree by ``__graft_entry__.build()``)."""
+    global _cache_lib
+    if _cache_lib is None:
+        if not os.path.exists(CACHE_LIB_PATH):
+            raise ImportError(f"{CACHE_LIB_PATH} is missing: run __graft_entry__.build() first")
+        L = ctypes.CDLL(CACHE_LIB_PATH)
+        P, I, Z, Q = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+        L.spec_cache_page_bytes.argtypes = [I, I, I]
+        L.spec_cache_page_bytes.restype = Z
+        L.spec_cache_attend_workspace_size.argtypes = [I, I, I, I, I]
+        L.spec_cache_attend_workspace_size.restype = Z
+        L.spec_cache_attend.argtypes = [P, Q, P, P, Q, P, P, I, I, I, ctypes.c_float, P, P, P, Z, P, P, P]
+        L.spec_cache_attend.restype = I
+        L.spec_cache_append.argtypes = [P, P, P, Q, I, I, P, P, I, P, P]
+        L.spec_cache_append.restype = I
+        L.spec_cache_read.argtypes = [P, I, I, P, P, P, P]
+        L.spec_cache_read.restype = I
+        _cache_lib = L
+    return _cache_lib
+
+
+def _fail(status: int, what: str):
+    from . import SpecVerifyError
+
+    raise SpecVerifyError(status, what)
+
+
+def spec_cache_page_bytes(kv_heads, page_size, head_dim) -> int:
+    """Bytes of one page; 0 on invalid sizes."""
+    return int(cache_lib().spec_cache_page_bytes(int(kv_heads), int(page_size), int(head_dim)))
+
+
+def spec_cache_attend_workspace_size(B, n, q_heads, kv_heads, head_dim) -> int:
+    """Workspace bytes of ``spec_cache_attend`` on the current device; 0 on invalid sizes."""
+    return int(cache_lib().spec_cache_attend_workspace_size(int(B), int(n), int(q_heads), int(kv_heads),
+                                                            int(head_dim)))
+
+
+def spec_cache_attend(q, q_stride, k_new, v_new, kv_stride, parents, cache: SvCache, B, n, q_heads, scale, out,
+                      out_lse=None, workspace=None, workspace_bytes=0, opts=None, out_status=None,
+                      stream=None) -> int:
+    from . import _opts, _p, _stream
+
+    return cache_lib().spec_cache_attend(_p(q), int(q_stride), _p(k_new), _p(v_new), int(kv_stride), _p(parents),
+                                         ctypes.byref(cache), int(B), int(n), int(q_heads), float(scale), _p(out),
+                                         _p(out_lse), _p(workspace), int(workspace_bytes), _opts(opts),
+                                         _p(out_status), _stream(stream))
+
+
+def spec_cache_append(cache: SvCache, k, v, kv_stride, B, n, n_accepted, nodes, nodes_stride, out_lens,
+                      stream=None) -> int:
+    from . import _p, _stream
+
+    return cache_lib().spec_cache_append(ctypes.byref(cache), _p(k), _p(v), int(kv_stride), int(B), int(n),
+                                         _p(n_accepted), _p(nodes), int(nodes_stride), _p(out_lens),
+                                         _stream(stream))
+
+
+def spec_cache_read(cache: SvCache, B, n, first, out_k, out_v, stream=None) -> int:
+    from . import _p, _stream
+
+    return cache_lib().spec_cache_read(ctypes.byref(cache), int(B), int(n), _p(first), _p(out_k), _p(out_v),
+                                       _stream(stream))
+
+
+class KvCache:
+    """The pages of a 4-bit cache.  ``pages`` is a contiguous uint8 tensor
+    [num_pages, kv_heads, page_size * (head_dim + 8)] on the GPU (the layout is
+    in ``spec_cache.h``), ``dtype`` the type of the activations and of the
+    parameters beside the codes: torch.bfloat16 or torch.float16."""
+
+    def __init__(self, pages, head_dim: int, dtype=None):
+        import torch
+
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+        if pages.dtype != torch.uint8:
+            raise TypeError(f"pages must be uint8, got {pages.dtype}")
+        if head_dim not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+        if pages.dim() != 3 or pages.shape[2] % (head_dim + 8) or not pages.is_contiguous() or pages.numel() == 0:
+            raise ValueError(f"pages must be contiguous [num_pages, kv_heads, page_size * {head_dim + 8}], got "
+                             f"{tuple(pages.shape)}")
+        size = pages.shape[2] // (head_dim + 8)
+        if not 16 <= size <= 1024 or size & (size - 1):
+            raise ValueError(f"page_size must be a power of two in [16, 1024], got {size}")
+        self.pages, self.head_dim, self.dtype = pages, int(head_dim), dtype
+        self.num_pages, self.kv_heads, self.page_size = pages.shape[0], pages.shape[1], size
+        self.device = pages.device
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=None, device="cuda"):
+        """A cache of ``num_pages`` unwritten pages."""
+        import torch
+
+        return cls(torch.zeros((num_pages, kv_heads, page_size * (head_dim + 8)), dtype=torch.uint8, device=device),
+                   head_dim, dtype)
+
+    def struct(self, page_table, lens) -> SvCache:
+        """``sv_cache_t`` of the pages with one batch's page table [B, max_pages]
+        and lengths [B] (int32).  Keep the tensors alive until the call completes."""
+        import torch
+
+        code = SV_DTYPE_F16 if self.dtype == torch.float16 else 0
+        return SvCache(self.pages.data_ptr(), page_table.data_ptr(), lens.data_ptr(), self.num_pages,
+                       page_table.shape[1], self.page_size, self.kv_heads, self.head_dim, code)
+
+
+def _ints(t, name, shape, device):
+    import torch
+
+    if not hasattr(t, "data_ptr"):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the pages on {device}")
+
+
+def _tokens(t, name, cache, heads=None):
+    """Checks activations [B, n, heads, D] whose heads lie side by side and
+    whose tokens are evenly spaced (a part of a fused projection's rows will
+    do); returns the elements between tokens."""
+    if not hasattr(t, "data_ptr"):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != cache.dtype:
+        raise TypeError(f"{name} must be {cache.dtype} like the cache, got {t.dtype}")
+    if t.dim() != 4 or t.shape[3] != cache.head_dim or (heads is not None and t.shape[2] != heads) or t.numel() == 0:
+        raise ValueError(f"{name} must be [B, n, {heads or 'heads'}, {cache.head_dim}], got shape {tuple(t.shape)}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the pages on {cache.device}")
+    (B, n, H, D), (sb, sn, sh, sd) = t.shape, t.stride()
+    step = sn if n > 1 else sb if B > 1 else H * D
+    if sd != 1 or (H > 1 and sh != D) or (n > 1 and B > 1 and sb != n * sn) or step < H * D:
+        raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, got strides {t.stride()}")
+    if step % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name}: tokens must be 16-byte aligned")
+    return step
+
+
+def _batch(cache, page_table, lens, B):
+    import torch
+
+    if not isinstance(cache, KvCache):
+        raise TypeError("cache must be a KvCache")
+    if cache.device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {cache.device}")
+    _ints(lens, "lens", (B,), cache.device)
+    if not hasattr(page_table, "data_ptr") or page_table.dim() != 2 or page_table.shape[1] < 1:
+        raise ValueError("page_table must be a [B, max_pages] tensor")
+    _ints(page_table, "page_table", (B, page_table.shape[1]), cache.device)
+
+
+@contextlib.contextmanager
+def _nested(*managers):
+    with contextlib.ExitStack() as stack:
+        for m in managers:
+            stack.enter_context(m)
+        yield
+
+
+def _on(device, stream):
+    """(context, raw stream): the pages' device is made current where it is
+    not, and what the call allocates belongs to the stream it runs on."""
+    import torch
+
+    managers = []
+    if device.index is not None and device.index != torch.cuda.current_device():
+        managers.append(torch.cuda.device(device))
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    else:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        raw = stream.cuda_stream
+        managers.append(torch.cuda.stream(stream))
+    return (_nested(*managers) if managers else contextlib.nullcontext()), raw
+
+
+def cache_attend(q, cache: KvCache, page_table, lens, k=None, v=None, parents=None, scale: Optional[float] = None,
+                 out=None, out_lse=None, out_status=None, workspace=None, opts=None, stream=None):
+    """Attention of the scored positions: q [B, n, q_heads, D] over each
+    sequence's ``lens`` cached tokens and, with ``k`` and ``v`` [B, n, kv_heads,
+    D], over the positions themselves: node i sees itself and its ancestors,
+    ``parents`` [B, n-1] int32 as for ``verify_tree`` or None for a chain.
+    Without k and v every position sees the cached tokens alone.  ``scale``
+    defaults to 1 / sqrt(D).  ``page_table`` [B, max_pages] and ``lens`` [B]
+    int32.  Optional: out [B, n, q_heads, D], out_lse [B, n, q_heads] fp32,
+    out_status [1] int32, workspace (uint8, allocated with torch when None; calls
+    that can overlap need one each).  Returns out."""
+    import torch
+
+    B, n = q.shape[:2] if hasattr(q, "data_ptr") and q.dim() == 4 else (0, 0)
+    _batch(cache, page_table, lens, B)
+    dev, D = cache.device, cache.head_dim
+    q_step = _tokens(q, "q", cache)
+    Hq = q.shape[2]
+    if Hq % cache.kv_heads:
+        raise ValueError(f"{Hq} query heads are no multiple of {cache.kv_heads} key/value heads")
+    if n > 257:
+        raise ValueError(f"at most 257 positions per sequence, got {n}")
+    if (k is None) != (v is None):
+        raise ValueError("k and v come together")
+    kv_step = 0
+    if k is not None:
+        kv_step = _tokens(k, "k", cache, cache.kv_heads)
+        if k.shape[:2] != (B, n) or v.shape[:2] != (B, n):
+            raise ValueError(f"k and v must have the tokens of q: {tuple(k.shape)}, {tuple(v.shape)}")
+        if _tokens(v, "v", cache, cache.kv_heads) != kv_step:
+            raise ValueError("k and v must have the same strides")
+    if parents is not None:
+        _ints(parents, "parents", (B, n - 1), dev)
+    if out is not None:
+        if out.dtype != cache.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
+            raise ValueError(f"out must be contiguous {cache.dtype} {list(q.shape)} on {dev}")
+    if out_lse is not None:
+        if out_lse.dtype != torch.float32 or out_lse.shape != (B, n, Hq) or not out_lse.is_contiguous() or \
+                out_lse.device != dev:
+            raise ValueError(f"out_lse must be contiguous torch.float32 {[B, n, Hq]} on {dev}")
+    if out_status is not None:
+        _ints(out_status, "out_status", (1,), dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    context, raw = _on(dev, stream)
+    with context:
+        if out is None:
+            out = torch.empty((B, n, Hq, D), dtype=cache.dtype, device=dev)
+        if workspace is None:
+            need = cache_lib().spec_cache_attend_workspace_size(B, n, Hq, cache.kv_heads, D)
+            if need == 0:
+                _fail(-2, "spec_cache_attend_workspace_size")
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        st = cache_lib().spec_cache_attend(
+            q.data_ptr(), q_step, None if k is None else k.data_ptr(), None if v is None else v.data_ptr(), kv_step,
+            None if parents is None or n == 1 else parents.data_ptr(), ctypes.byref(cache.struct(page_table, lens)),
+            B, n, Hq, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(),
+            None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), None if opts is None else ctypes.byref(opts),
+            None if out_status is None else out_status.data_ptr(), raw)
+    if st != 0:
+        _fail(st, "spec_cache_attend")
+    return out
+
+
+def cache_append(cache: KvCache, page_table, lens, k, v, n_accepted=None, nodes=None, out_lens=None, stream=None):
+    """Quantise kept rows of k and v [B, n, kv_heads, D] behind each sequence's
+    ``lens`` tokens.  ``n_accepted`` [B] int32: sequence b keeps 1 +
+    n_accepted[b] rows (the count ``verify`` returns; -1 keeps none), None all
+    n.  ``nodes`` [B, >= n-1] int32: row i is node nodes[b][i-1] (the
+    ``out_nodes`` of ``verify_tree``), None row i.  ``out_lens`` [B] int32 may be
+    ``lens`` itself, which is then advanced in place; a new tensor when None.
+    Returns the new lengths (-1: a data error of that sequence)."""
+    import torch
+
+    B, n = k.shape[:2] if hasattr(k, "data_ptr") and k.dim() == 4 else (0, 0)
+    _batch(cache, page_table, lens, B)
+    dev = cache.device
+    step = _tokens(k, "k", cache, cache.kv_heads)
+    if _tokens(v, "v", cache, cache.kv_heads) != step or v.shape != k.shape:
+        raise ValueError(f"v must have the shape and strides of k: {tuple(v.shape)}, {tuple(k.shape)}")
+    if n_accepted is not None:
+        _ints(n_accepted, "n_accepted", (B,), dev)
+    stride = 0
+    if nodes is not None:
+        if not hasattr(nodes, "data_ptr") or nodes.dim() != 2 or nodes.shape[1] < n - 1:
+            raise ValueError(f"nodes must be [B, >= {n - 1}]")
+        _ints(nodes, "nodes", (B, nodes.shape[1]), dev)
+        stride = nodes.shape[1]
+    if out_lens is not None:
+        _ints(out_lens, "out_lens", (B,), dev)
+    context, raw = _on(dev, stream)
+    with context:
+        if out_lens is None:
+            out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        st = cache_lib().spec_cache_append(
+            ctypes.byref(cache.struct(page_table, lens)), k.data_ptr(), v.data_ptr(), step, B, n,
+            None if n_accepted is None else n_accepted.data_ptr(),
+            None if nodes is None or stride == 0 else nodes.data_ptr(), stride, out_lens.data_ptr(), raw)
+    if st != 0:
+        _fail(st, "spec_cache_append")
+    return out_lens
+
+
+def cache_read(cache: KvCache, page_table, lens, n: int, first=None, out_k=None, out_v=None, stream=None):
+    """Positions first[b] .. first[b] + n - 1 of every sequence (``first`` [B]
+    int32, None: 0) as (k, v), each [B, n, kv_heads, D] in the cache's type;
+    rows outside a sequence's ``lens`` tokens are zeros."""
+    import torch
+
+    B = lens.shape[0] if hasattr(lens, "data_ptr") and lens.dim() == 1 else 0
+    _batch(cache, page_table, lens, B)
+    dev = cache.device
+    if n < 1 or B < 1:
+        raise ValueError("nothing to read")
+    if first is not None:
+        _ints(first, "first", (B,), dev)
+    shape = (B, n, cache.kv_heads, cache.head_dim)
+    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
+        if t is not None and (t.dtype != cache.dtype or t.shape != shape or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{name} must be contiguous {cache.dtype} {list(shape)} on {dev}")
+    context, raw = _on(dev, stream)
+    with context:
+        if out_k is None:
+            out_k = torch.empty(shape, dtype=cache.dtype, device=dev)
+        if out_v is None:
+            out_v = torch.empty(shape, dtype=cache.dtype, device=dev)
+        st = cache_lib().spec_cache_read(ctypes.byref(cache.struct(page_table, lens)), B, n,
+                                         None if first is None else first.data_ptr(), out_k.data_ptr(),
+                                         out_v.data_ptr(), raw)
+    if st != 0:
+        _fail(st, "spec_cache_read")
+    return out_k, out_v

@@ -1,0 +1,124 @@
+// Shared definitions of the 4-bit cache's kernels: the layout of a block, the
+// 16-bit types, and the expansion of 4-bit codes to tensor-core operands.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sv_ptx.cuh"
+
+namespace sv {
+
+constexpr float SC_NEG_INF = -__builtin_huge_valf();
+constexpr float SC_LOG2E = 1.4426950408889634f;
+constexpr float SC_LN2 = 0.6931471805599453f;
+constexpr int SC_BLOCK = 64;       // tokens of a block at most, and of a tile
+constexpr int SC_MAX_NODES = 257;  // node 0 and at most 256 drafts, as in tree verification
+
+// The cache as the kernels take it.
+struct CacheView {
+    unsigned char* pages;
+    const int32_t* table;
+    const int32_t* lens;
+    int num_pages, max_pages, page_size, kv_heads;
+    int block;      // T = min(page_size, 64)
+    int log2_block;
+    int log2_page;
+};
+
+// Bytes of a block's key half (and of its value half): T * D / 2 code bytes
+// and T (scale, zero) pairs of 4 bytes.
+template <int D>
+__host__ __device__ constexpr int sc_half_bytes(int T) {
+    return T * (D / 2 + 4);
+}
+
+// Address of a block: `id` is the page, `sub` the block within it.
+template <int D>
+__device__ __forceinline__ unsigned char* sc_block_ptr(const CacheView& c, int id, int head, int sub) {
+    const int per_page = c.page_size >> c.log2_block;
+    return c.pages + ((static_cast<size_t>(id) * c.kv_heads + head) * per_page + sub) *
+                         static_cast<size_t>(2 * sc_half_bytes<D>(c.block));
+}
+
+// Capacity of a sequence in tokens.
+__device__ __forceinline__ long long sc_capacity(const CacheView& c) {
+    return static_cast<long long>(c.max_pages) << c.log2_page;
+}
+
+// ---- the 16-bit types ---------------------------------------------------------
+
+template <int DT>
+struct SC;
+
+template <>
+struct SC<0> {  // bf16
+    using T = __nv_bfloat16;
+    static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {  // a in the low half
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    }
+    static __device__ __forceinline__ float round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+};
+
+template <>
+struct SC<1> {  // fp16
+    using T = __half;
+    static __device__ __forceinline__ float lo(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffffu)); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    }
+    static __device__ __forceinline__ float round(float x) { return __half2float(__float2half_rn(x)); }
+};
+
+// ---- 4-bit codes to operands --------------------------------------------------
+
+// Codes 2j and 2j+1 of a word as the bf16 pair (128 + code): a code placed in
+// the low mantissa bits of 128.0 is that sum exactly.
+__device__ __forceinline__ uint32_t sc_codes_bf16(uint32_t w, int j) {
+    return ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+}
+// The same as fp16 pairs (1024 + code).
+__device__ __forceinline__ uint32_t sc_codes_f16(uint32_t w, int j) {
+    return ((w >> (4 * j)) & 0x000F000Fu) | 0x64006400u;
+}
+// (128 + code) - 136 = code - 8, exact in bf16.
+__device__ __forceinline__ uint32_t sc_center_bf16(uint32_t x) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0xC308C308u));
+    return r;
+}
+// (1024 + code) - 1032 = code - 8, exact in fp16.
+__device__ __forceinline__ uint32_t sc_center_f16(uint32_t x) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0xE408E408u));
+    return r;
+}
+
+// m16n8k16 on the tensor cores, fp32 accumulators.
+template <int DT>
+__device__ __forceinline__ void sc_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (DT == 0)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+}  // namespace sv

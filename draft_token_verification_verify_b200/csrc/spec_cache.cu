@@ -1,0 +1,323 @@
+// Host side of the spec_cache C ABI: argument checks and launches.  Nothing
+// here allocates device memory or synchronises the caller's stream.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "../../include/spec_cache.h"
+#include "sc_attend.cuh"
+#include "sc_store.cuh"
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
+constexpr int kMaxPage = 1024;
+
+struct DeviceInfo {
+    bool ok = false;
+    int sms = 0;
+};
+
+DeviceInfo g_dev[kMaxDevices];
+std::once_flag g_dev_once[kMaxDevices];
+std::once_flag g_attr_once[kMaxDevices];
+cudaError_t g_attr_err[kMaxDevices];
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
+
+const DeviceInfo* device_info(int* dev_out) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    std::call_once(g_dev_once[dev], [dev] {
+        int major = 0, minor = 0;
+        DeviceInfo& d = g_dev[dev];
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return;
+        }
+        d.ok = major == 10 && minor == 0;  // sm_100a code runs on 10.0 only
+    });
+    *dev_out = dev;
+    return g_dev[dev].ok ? &g_dev[dev] : nullptr;
+}
+
+sv_status_t launched(cudaError_t e) {
+    if (e == cudaSuccess) return SV_OK;
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+}
+
+bool page_size_ok(int p) { return p >= 16 && p <= kMaxPage && (p & (p - 1)) == 0; }
+int log2_of(int x) { return 31 - __builtin_clz(static_cast<unsigned>(x)); }
+
+sv_status_t check_cache(const sv_cache_t* c, sv::CacheView* v, int* dt) {
+    if (!c || !c->pages || !c->page_table || !c->lens || !aligned(c->pages, 16) || !aligned(c->page_table, 4) ||
+        !aligned(c->lens, 4) || c->num_pages <= 0 || c->max_pages <= 0 || !page_size_ok(c->page_size) ||
+        c->kv_heads <= 0 || c->head_dim <= 0)
+        return SV_ERR_INVALID_ARG;
+    if (c->dtype != SV_DTYPE_BF16 && c->dtype != SV_DTYPE_F16) return SV_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return SV_ERR_UNSUPPORTED;
+    // positions are counted in 32 bits
+    if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 30) || c->kv_heads > 65536)
+        return SV_ERR_UNSUPPORTED;
+    v->pages = static_cast<unsigned char*>(c->pages);
+    v->table = c->page_table;
+    v->lens = c->lens;
+    v->num_pages = c->num_pages;
+    v->max_pages = c->max_pages;
+    v->page_size = c->page_size;
+    v->kv_heads = c->kv_heads;
+    v->block = c->page_size < sv::SC_BLOCK ? c->page_size : sv::SC_BLOCK;
+    v->log2_block = log2_of(v->block);
+    v->log2_page = log2_of(c->page_size);
+    *dt = c->dtype == SV_DTYPE_F16 ? 1 : 0;
+    return SV_OK;
+}
+
+// ---- the attention's plan ---------------------------------------------------------
+
+struct Plan {
+    int grid = 0, block_rows = 0, row_blocks = 0;
+    size_t off_ml = 0, off_desc = 0, bytes = 0;
+};
+
+bool make_plan(const DeviceInfo& d, int B, int n, int q_heads, int kv_heads, int D, Plan* p) {
+    const long long rows = static_cast<long long>(n) * (q_heads / kv_heads);
+    if (rows > (1 << 24)) return false;
+    p->block_rows = sv::SC_ROWS;
+    p->row_blocks = static_cast<int>(ceil_div(rows, p->block_rows));
+    p->grid = 2 * d.sms;
+    const size_t parts = static_cast<size_t>(p->grid) * 2 * p->block_rows;
+    p->off_ml = round_up(parts * D * sizeof(float), 256);
+    p->off_desc = p->off_ml + round_up(parts * sizeof(float2), 256);
+    p->bytes = p->off_desc + round_up(static_cast<size_t>(p->grid) * sizeof(int4), 256);
+    return static_cast<long long>(B) * kv_heads * p->row_blocks <= (1LL << 31);
+}
+
+bool attend_sizes_ok(int B, int n, int q_heads, int kv_heads) {
+    return B > 0 && n >= 1 && n <= sv::SC_MAX_NODES && kv_heads > 0 && q_heads > 0 && q_heads % kv_heads == 0;
+}
+
+using AttendFn = void (*)(sv::AttendParams);
+using JoinFn = void (*)(sv::AttendParams, int, int);
+
+AttendFn pick_attend(int dt, int D) {
+    if (D == 64) return dt ? sv::sc_attend_kernel<1, 64> : sv::sc_attend_kernel<0, 64>;
+    return dt ? sv::sc_attend_kernel<1, 128> : sv::sc_attend_kernel<0, 128>;
+}
+JoinFn pick_join(int dt, int D) {
+    if (D == 64) return dt ? sv::sc_join_kernel<1, 64> : sv::sc_join_kernel<0, 64>;
+    return dt ? sv::sc_join_kernel<1, 128> : sv::sc_join_kernel<0, 128>;
+}
+
+sv_status_t set_attrs(int dev) {
+    std::call_once(g_attr_once[dev], [dev] {
+        cudaError_t e = cudaSuccess;
+        for (int dt = 0; dt < 2; ++dt)
+            for (int D = 64; D <= 128; D += 64) {
+                const int bytes = D == 64 ? sv::AttendSmem<64>::BYTES : sv::AttendSmem<128>::BYTES;
+                const cudaError_t x = cudaFuncSetAttribute(reinterpret_cast<const void*>(pick_attend(dt, D)),
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                if (x != cudaSuccess) e = x;
+            }
+        if (e != cudaSuccess) cudaGetLastError();
+        g_attr_err[dev] = e;
+    });
+    return g_attr_err[dev] == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+bool strides_ok(const void* p, long long stride, long long width) {
+    return aligned(p, 16) && stride >= width && stride % 8 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_cache_page_bytes(int kv_heads, int page_size, int head_dim) {
+    if (kv_heads <= 0 || kv_heads > 65536 || !page_size_ok(page_size) || (head_dim != 64 && head_dim != 128)) return 0;
+    return static_cast<size_t>(kv_heads) * page_size * (head_dim + 8);
+}
+
+size_t spec_cache_attend_workspace_size(int B, int n, int q_heads, int kv_heads, int head_dim) {
+    if (!attend_sizes_ok(B, n, q_heads, kv_heads) || (head_dim != 64 && head_dim != 128)) return 0;
+    int dev = 0;
+    const DeviceInfo* d = device_info(&dev);
+    Plan p;
+    return d && make_plan(*d, B, n, q_heads, kv_heads, head_dim, &p) ? p.bytes : 0;
+}
+
+sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_new, const void* v_new,
+                              long long kv_stride, const int32_t* parents, const sv_cache_t* cache, int B, int n,
+                              int q_heads, float scale, void* out, float* out_lse, void* workspace,
+                              size_t workspace_bytes, const sv_options_t* opts, int32_t* out_status, void* stream) {
+    sv::AttendParams P;
+    std::memset(&P, 0, sizeof P);
+    int dt = 0;
+    const sv_status_t s = check_cache(cache, &P.c, &dt);
+    if (s != SV_OK) return s;
+    const int D = cache->head_dim;
+    if (!attend_sizes_ok(B, n, q_heads, cache->kv_heads) || !std::isfinite(scale)) return SV_ERR_INVALID_ARG;
+    if (!q || !out || !workspace || (k_new == nullptr) != (v_new == nullptr)) return SV_ERR_INVALID_ARG;
+    if (!strides_ok(q, q_stride, static_cast<long long>(q_heads) * D) || !aligned(out, 16) ||
+        !aligned(workspace, 16) || (out_lse && !aligned(out_lse, 4)) || (parents && !aligned(parents, 4)) ||
+        (out_status && !aligned(out_status, 4)))
+        return SV_ERR_INVALID_ARG;
+    if (k_new && (!strides_ok(k_new, kv_stride, static_cast<long long>(cache->kv_heads) * D) || !aligned(v_new, 16)))
+        return SV_ERR_INVALID_ARG;
+    if (opts && (opts->top_p || opts->vocab_mask || opts->rep_ids)) return SV_ERR_UNSUPPORTED;
+    int dev = 0;
+    const DeviceInfo* info = device_info(&dev);
+    if (!info) return SV_ERR_UNSUPPORTED;
+    Plan plan;
+    if (!make_plan(*info, B, n, q_heads, cache->kv_heads, D, &plan)) return SV_ERR_UNSUPPORTED;
+    if (workspace_bytes < plan.bytes) return SV_ERR_INVALID_ARG;
+    const sv_status_t sa = set_attrs(dev);
+    if (sa != SV_OK) return sa;
+
+    P.q = q;
+    P.q_stride = q_stride;
+    P.k_new = k_new;
+    P.v_new = v_new;
+    P.kv_stride = kv_stride;
+    P.parents = k_new && n > 1 ? parents : nullptr;
+    P.B = B;
+    P.n = n;
+    P.q_heads = q_heads;
+    P.group = q_heads / cache->kv_heads;
+    P.rows = n * P.group;
+    P.row_blocks = plan.row_blocks;
+    P.scale = scale;
+    P.out = out;
+    P.out_lse = out_lse;
+    auto* ws = static_cast<unsigned char*>(workspace);
+    P.part_o = reinterpret_cast<float*>(ws);
+    P.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+    P.desc = reinterpret_cast<int4*>(ws + plan.off_desc);
+    P.timeout_ns = (opts && opts->wait_timeout_ns) ? opts->wait_timeout_ns : kDefaultTimeoutNs;
+    P.test_hook = (opts && opts->test_extra_tx) ? 1 : 0;
+    P.out_status = out_status;
+
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (opts && opts->event_start) {
+        const sv_status_t e = launched(cudaEventRecord(static_cast<cudaEvent_t>(opts->event_start), st));
+        if (e != SV_OK) return e;
+    }
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), 1, 1);
+    cfg.blockDim = dim3(sv::SC_NT, 1, 1);
+    cfg.dynamicSmemBytes = D == 64 ? sv::AttendSmem<64>::BYTES : sv::AttendSmem<128>::BYTES;
+    cfg.stream = st;
+    sv_status_t r = launched(cudaLaunchKernelEx(&cfg, pick_attend(dt, D), P));
+    if (r != SV_OK) return r;
+    if (opts && opts->event_stop) {
+        r = launched(cudaEventRecord(static_cast<cudaEvent_t>(opts->event_stop), st));
+        if (r != SV_OK) return r;
+    }
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), static_cast<unsigned>(plan.block_rows / 4), 1);
+    cfg.blockDim = dim3(sv::SC_JOIN_NT, 1, 1);
+    cfg.stream = st;
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    return launched(cudaLaunchKernelEx(&cfg, pick_join(dt, D), P, plan.grid, plan.block_rows));
+}
+
+sv_status_t spec_cache_append(const sv_cache_t* cache, const void* k, const void* v, long long kv_stride, int B,
+                              int n, const int32_t* n_accepted, const int32_t* nodes, int nodes_stride,
+                              int32_t* out_lens, void* stream) {
+    sv::CacheView c;
+    int dt = 0;
+    const sv_status_t s = check_cache(cache, &c, &dt);
+    if (s != SV_OK) return s;
+    const int D = cache->head_dim;
+    if (B <= 0 || n < 1 || !k || !v || !out_lens || !strides_ok(k, kv_stride, static_cast<long long>(c.kv_heads) * D) ||
+        !aligned(v, 16) || (n_accepted && !aligned(n_accepted, 4)) || (nodes && !aligned(nodes, 4)) ||
+        !aligned(out_lens, 4) || (nodes && nodes_stride < n - 1))
+        return SV_ERR_INVALID_ARG;
+    const bool in_place = out_lens == cache->lens;
+    if (!in_place && out_lens < cache->lens + B && cache->lens < out_lens + B) return SV_ERR_INVALID_ARG;
+    int dev = 0;
+    if (!device_info(&dev)) return SV_ERR_UNSUPPORTED;
+    sv::AppendParams P;
+    P.k = k;
+    P.v = v;
+    P.stride = kv_stride;
+    P.B = B;
+    P.n = n;
+    P.n_accepted = n_accepted;
+    P.nodes = nodes;
+    P.nodes_stride = nodes_stride;
+    P.out_lens = in_place ? nullptr : out_lens;
+    P.nblk = static_cast<int>((static_cast<long long>(n) + c.block - 2) / c.block + 1);
+    const long long items = static_cast<long long>(B) * P.nblk * c.kv_heads;
+    const long long blocks = ceil_div(items, sv::SC_STORE_NT / (D / 4));
+    if (blocks > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void (*fn)(sv::CacheView, sv::AppendParams) =
+        D == 64 ? (dt ? sv::sc_append_kernel<1, 64> : sv::sc_append_kernel<0, 64>)
+                : (dt ? sv::sc_append_kernel<1, 128> : sv::sc_append_kernel<0, 128>);
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(sv::SC_STORE_NT, 1, 1);
+    cfg.stream = st;
+    sv_status_t r = launched(cudaLaunchKernelEx(&cfg, fn, c, P));
+    if (r != SV_OK || !in_place) return r;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(B, sv::SC_STORE_NT / 32)), 1, 1);
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    return launched(cudaLaunchKernelEx(&cfg, sv::sc_advance_kernel, c, P, out_lens));
+}
+
+sv_status_t spec_cache_read(const sv_cache_t* cache, int B, int n, const int32_t* first, void* out_k, void* out_v,
+                            void* stream) {
+    sv::CacheView c;
+    int dt = 0;
+    const sv_status_t s = check_cache(cache, &c, &dt);
+    if (s != SV_OK) return s;
+    const int D = cache->head_dim;
+    if (B <= 0 || n < 1 || (!out_k && !out_v) || (out_k && !aligned(out_k, 16)) || (out_v && !aligned(out_v, 16)) ||
+        (first && !aligned(first, 4)))
+        return SV_ERR_INVALID_ARG;
+    int dev = 0;
+    if (!device_info(&dev)) return SV_ERR_UNSUPPORTED;
+    sv::ReadParams P;
+    P.first = first;
+    P.out_k = out_k;
+    P.out_v = out_v;
+    P.B = B;
+    P.n = n;
+    P.nblk = static_cast<int>((static_cast<long long>(n) + c.block - 2) / c.block + 1);
+    const long long items = static_cast<long long>(B) * P.nblk * c.kv_heads;
+    const long long blocks = ceil_div(items, sv::SC_STORE_NT / (D / 4));
+    if (blocks > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+    void (*fn)(sv::CacheView, sv::ReadParams) = D == 64 ? (dt ? sv::sc_read_kernel<1, 64> : sv::sc_read_kernel<0, 64>)
+                                                        : (dt ? sv::sc_read_kernel<1, 128> : sv::sc_read_kernel<0, 128>);
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(sv::SC_STORE_NT, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    return launched(cudaLaunchKernelEx(&cfg, fn, c, P));
+}
+
+}  // extern "C"

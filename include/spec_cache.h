@@ -1,0 +1,162 @@
+/*
+ * spec_cache — a paged key/value cache held in 4 bits beside speculative
+ * verification, on NVIDIA B200 (sm_100a).  C ABI of libspec_cache.so; every
+ * entry point is asynchronous on the caller's CUDA stream and allocates
+ * nothing.
+ *
+ * A round of speculative decoding scores k+1 positions per sequence, verifies
+ * them (spec_verify.h) and keeps the accepted ones.  These calls are the two
+ * steps on either side of the verification that depend on the draft's shape:
+ *   spec_cache_attend  attention of the scored positions over the cached
+ *                      context and over the positions themselves, chain or
+ *                      tree (the parents of spec_verify_tree);
+ *   spec_cache_append  the accepted positions' keys and values quantised into
+ *                      the cache, as out_n_accepted (and out_nodes) of the
+ *                      verification say, without a decision on the host;
+ *   spec_cache_read    a range of every sequence read back.
+ *
+ * What the cache holds.  A row x[0..D) of one token and key/value head is
+ * written as
+ *   zero  = min x
+ *   scale = (max x - min x) / 15 in fp32, rounded to the cache's 16-bit type
+ *   code  = round((x - zero) / scale) to nearest, ties to even, in fp32,
+ *           clamped to 0..15 (0 where scale is 0)
+ * and stands for zero + scale * code.  A row that holds a NaN or an infinity,
+ * or whose range or scale is not finite, is written with scale = NaN: every
+ * element of it reads back as NaN, and so does every attention output that
+ * reads it.
+ *
+ * Layout.  A page holds page_size tokens of every key/value head; a block is
+ * T = min(page_size, 64) tokens of one head:
+ *   pages [num_pages][kv_heads][page_size / T][T * (D + 8) bytes]
+ *   block T rows of D/2 bytes   key codes: the little-endian 32-bit word w of
+ *                               a row holds the dims 8w..8w+7, dim 8w+2i in
+ *                               bits 4i..4i+3, dim 8w+2i+1 in bits
+ *                               16+4i..19+4i (i = 0..3)
+ *         T pairs (scale, zero) the keys' parameters, 16-bit type
+ *         D rows of T/2 bytes   value codes: row d, the block's tokens in the
+ *                               same order within each word
+ *         T pairs (scale, zero) the values' parameters
+ *
+ * Errors.  Argument problems found on the host return SV_ERR_INVALID_ARG with
+ * no launch; SV_ERR_UNSUPPORTED: the current device is not of compute
+ * capability 10.0, or a size that the kernels do not take (below);
+ * SV_ERR_CUDA: a launch failed.  Data errors of one sequence do not fail the
+ * call and are stated at each entry point.  Pointers are device memory owned
+ * by the caller, valid until the stream work completes.
+ */
+#ifndef SPEC_CACHE_H
+#define SPEC_CACHE_H
+
+#include "spec_verify.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The cache's and the activations' type: SV_DTYPE_BF16 or this. */
+enum { SV_DTYPE_F16 = 2 << 8 };
+
+typedef struct sv_cache {
+    void* pages;               /* the pages, 16-byte aligned */
+    const int32_t* page_table; /* [B][max_pages]: the page that holds the tokens p * page_size
+                                  and up of sequence b; entries past a sequence's length are
+                                  not read.  Sequences may share pages that are only read */
+    const int32_t* lens;       /* [B]: cached tokens of each sequence; negative: no sequence */
+    int num_pages;             /* > 0 */
+    int max_pages;             /* entries of a page-table row, > 0 */
+    int page_size;             /* tokens of a page: a power of two in [16, 1024] */
+    int kv_heads;              /* > 0 */
+    int head_dim;              /* D: 64 or 128 (SV_ERR_UNSUPPORTED otherwise) */
+    int dtype;                 /* SV_DTYPE_BF16 or SV_DTYPE_F16 */
+} sv_cache_t;
+
+/* Bytes of one page: kv_heads * page_size * (head_dim + 8); 0 on invalid sizes. */
+SV_API size_t spec_cache_page_bytes(int kv_heads, int page_size, int head_dim);
+
+/*
+ * spec_cache_attend — attention of n scored positions per sequence.
+ *   q            token b * n + i at q + (b * n + i) * q_stride elements, there
+ *                [q_heads][D]: node i of sequence b (node 0 the last verified
+ *                token, as in spec_verify_tree).  16-byte aligned; q_stride a
+ *                multiple of 8, >= q_heads * D
+ *   k_new, v_new the scored positions' own keys and values, [kv_heads][D] per
+ *                token, kv_stride likewise; both NULL: the cached context
+ *                alone (every position sees all of it)
+ *   parents      [B][n-1] int32 or NULL: the parent of node i is
+ *                parents[b][i-1] in [0, i), as in spec_verify_tree; NULL: a
+ *                chain.  Node i sees the cached tokens, itself and its
+ *                ancestors.  Ignored without k_new
+ *   B, n         sequences, positions per sequence (1..257)
+ *   q_heads      a multiple of kv_heads; query head h
+ *                reads key/value head h / (q_heads / kv_heads)
+ *   scale        multiplies q . k before the softmax; finite
+ *   out          [B][n][q_heads][D], the cache's type
+ *   out_lse      [B][n][q_heads] fp32 or NULL: log of the sum of exp(scale *
+ *                q . k) over the keys seen
+ *   workspace    spec_cache_attend_workspace_size bytes, 16-byte aligned,
+ *                written before it is read; calls that can overlap need one each
+ *   opts         NULL or options: wait_timeout_ns, event_start / event_stop
+ *                (around the attention kernel) and test_extra_tx (non-zero: no
+ *                copy is issued and every wait for one runs out); the
+ *                processors give SV_ERR_UNSUPPORTED
+ *   out_status   1 int32 or NULL: SV_OK, or SV_ERR_DEVICE_TIMEOUT when a
+ *                device-side wait ran out (its outputs are NaN)
+ * A position that sees no key (no k_new, an empty or absent sequence) gets
+ * zeros and an out_lse of -inf.  Data errors: a length above max_pages *
+ * page_size, a page outside [0, num_pages) that holds cached tokens, or a
+ * parent outside [0, i) makes the sequence's outputs NaN.
+ * Scores, softmax statistics and sums are held in fp32; the softmax weights
+ * are rounded to the 16-bit operand type of the tensor cores.  The split of
+ * the work, and with it the order of the sums, depends on the lengths and
+ * sizes alone: the same call gives the same bits.
+ */
+SV_API sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_new, const void* v_new,
+                                     long long kv_stride, const int32_t* parents, const sv_cache_t* cache, int B,
+                                     int n, int q_heads, float scale, void* out, float* out_lse, void* workspace,
+                                     size_t workspace_bytes, const sv_options_t* opts, int32_t* out_status,
+                                     void* stream);
+
+/* Workspace bytes of spec_cache_attend on the current device; 0 on invalid
+ * sizes or without a usable device. */
+SV_API size_t spec_cache_attend_workspace_size(int B, int n, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * spec_cache_append — quantise the kept rows behind each sequence's length.
+ *   k, v        [B][n] tokens of [kv_heads][D] in the cache's type; token
+ *               b * n + i at (b * n + i) * kv_stride elements (a multiple of
+ *               8, 16-byte aligned base)
+ *   n_accepted  [B] int32 or NULL: sequence b keeps 1 + n_accepted[b] rows
+ *               (the out_n_accepted of a verification; -1 keeps none); NULL:
+ *               all n rows
+ *   nodes       [B][nodes_stride] int32 or NULL: row 0 is node 0 and row i is
+ *               node nodes[b][i-1] (the out_nodes of spec_verify_tree, whose
+ *               stride is N + 1); NULL: row i is node i
+ *   out_lens    [B] int32: the new lengths.  May be cache->lens itself, but
+ *               must not overlap it otherwise
+ * Rows go to the positions lens[b], lens[b] + 1, ...; the page table must
+ * already map them, and the pages written must belong to one sequence alone.
+ * A negative length stays as it is and nothing is written.  Data errors: more
+ * than n rows, a node outside [0, n), a position past max_pages * page_size or
+ * on a page outside [0, num_pages) make out_lens[b] = -1 (the sequence's
+ * earlier tokens are untouched; what lies behind them is undefined).
+ */
+SV_API sv_status_t spec_cache_append(const sv_cache_t* cache, const void* k, const void* v, long long kv_stride,
+                                     int B, int n, const int32_t* n_accepted, const int32_t* nodes,
+                                     int nodes_stride, int32_t* out_lens, void* stream);
+
+/*
+ * spec_cache_read — positions first[b] .. first[b] + n - 1 of every sequence
+ * (first NULL: 0), each element rounded once to the cache's type.
+ *   out_k, out_v  [B][n][kv_heads][D], 16-byte aligned; either may be NULL
+ * Rows outside [0, lens[b]) are zeros; rows on a page outside [0, num_pages),
+ * or past max_pages * page_size, are NaN.
+ */
+SV_API sv_status_t spec_cache_read(const sv_cache_t* cache, int B, int n, const int32_t* first, void* out_k,
+                                   void* out_v, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SPEC_CACHE_H */
