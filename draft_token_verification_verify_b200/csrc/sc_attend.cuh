@@ -58,12 +58,14 @@ __device__ __forceinline__ int sc_len(const AttendParams& P, int b, bool* bad) {
     *bad = len > sc_capacity(P.c);
     return (len < 0 || *bad) ? 0 : len;
 }
+template <int TILE>
 __device__ __forceinline__ int sc_new_units(const AttendParams& P) {
-    return P.k_new ? (P.n + SC_BLOCK - 1) / SC_BLOCK : 0;
+    return P.k_new ? (P.n + TILE - 1) / TILE : 0;
 }
+template <int TILE>
 __device__ __forceinline__ int sc_units(const AttendParams& P, int b) {
     bool bad;
-    const int u = (sc_len(P, b, &bad) + SC_BLOCK - 1) / SC_BLOCK + sc_new_units(P);
+    const int u = (sc_len(P, b, &bad) + TILE - 1) / TILE + sc_new_units<TILE>(P);
     return u > 0 ? u : 1;
 }
 
@@ -74,7 +76,7 @@ struct Range {
     long long before;                // units before that sequence
 };
 
-template <int NT>
+template <int NT, int TILE>
 __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) {
     __shared__ long long scan[NT / 32];
     __shared__ long long found[2];
@@ -82,7 +84,7 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) 
     const int per = (P.B + NT - 1) / NT;
     const long long segs = static_cast<long long>(P.c.kv_heads) * P.row_blocks;
     long long mine = 0;
-    for (int b = tid * per; b < (tid + 1) * per && b < P.B; ++b) mine += sc_units(P, b);
+    for (int b = tid * per; b < (tid + 1) * per && b < P.B; ++b) mine += sc_units<TILE>(P, b);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -107,7 +109,7 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) 
     if (r.g0 < r.g1 && r.g0 >= at && r.g0 < at + mine * segs) {
         int b = tid * per;
         for (;; ++b) {
-            const long long u = sc_units(P, b) * segs;
+            const long long u = sc_units<TILE>(P, b) * segs;
             if (r.g0 < at + u) break;
             at += u;
         }
@@ -121,43 +123,47 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) 
     return r;
 }
 
-// A walk over the units of a range, `step` units at a time within a segment.
+// A walk over the parts of segments in a CTA's range.
+template <int TILE>
 struct Walk {
-    int b, hr;        // sequence; head * row_blocks + row block
-    int units, len;   // of the sequence
-    bool bad;
-    long long start;  // first unit of the segment
-    int u, u0, u1;    // unit of the segment; the range's share of it: [u0, u1)
+    int b, hr;       // sequence; head * row_blocks + row block
+    int units, len;  // of the sequence
+    int u0, u1;      // the range's share of the segment's units: [u0, u1)
+    int left;        // units of the range behind this part
+    int u;           // for the caller: the unit it is at
+    bool bad;        // a length above the capacity
 
-    __device__ __forceinline__ void enter(const AttendParams& P, const Range& r) {
-        u0 = static_cast<int>(r.g0 > start ? r.g0 - start : 0);
-        u1 = static_cast<int>(r.g1 < start + units ? r.g1 - start : units);
-    }
     __device__ __forceinline__ void sequence(const AttendParams& P) {
-        units = sc_units(P, b);
+        units = sc_units<TILE>(P, b);
         len = sc_len(P, b, &bad);
     }
     __device__ __forceinline__ void begin(const AttendParams& P, const Range& r) {
         b = r.b;
         sequence(P);
-        hr = static_cast<int>((r.g0 - r.before) / units);
-        start = r.before + static_cast<long long>(hr) * units;
-        enter(P, r);
+        const long long in = r.g0 - r.before;
+        hr = static_cast<int>(in / units);
+        u0 = static_cast<int>(in - static_cast<long long>(hr) * units);
+        left = static_cast<int>(r.g1 - r.g0);
+        u1 = units - u0 < left ? units : u0 + left;
+        left -= u1 - u0;
     }
     // The next segment; false behind the range.
-    __device__ __forceinline__ bool next(const AttendParams& P, const Range& r) {
-        start += units;
-        if (start >= r.g1) return false;
+    __device__ __forceinline__ bool next(const AttendParams& P) {
+        if (left <= 0) return false;
         if (++hr == P.c.kv_heads * P.row_blocks) {
             hr = 0;
             ++b;
             sequence(P);
         }
-        enter(P, r);
+        u0 = 0;
+        u1 = units < left ? units : left;
+        left -= u1;
         return true;
     }
     // Whether this part is the whole segment.
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
+    // CTAs that hold parts of a segment begun here and cut by the range's end.
+    __device__ __forceinline__ int parts(int chunk) const { return 1 + (units - u1 + chunk - 1) / chunk; }
 };
 
 // Row `r` of segment (b, head): its element offset in [B][n][q_heads].
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     const CacheView& c = P.c;
 
     pdl_launch_dependents();
-    const Range R = sc_range<SC_NT>(P, SC_MIN_TILES);
+    const Range R = sc_range<SC_NT, SC_BLOCK>(P, SC_MIN_TILES);
     int error = 0;
     if (tid == 0) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (R.g0 >= R.g1) return;
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     const float sl = P.scale * SC_LOG2E;
 
     // ---- the copies: tile `iw` of this warp is issued SC_STAGES tiles ahead ----
-    Walk iw;
+    Walk<SC_BLOCK> iw;
     iw.begin(P, R);
     iw.u = iw.u0 + warp;
     bool more = true;
@@ -222,7 +228,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     auto settle = [&]() {    // to the next cache tile at or behind iw.u
         while (more) {
             if (iw.u < iw.u1 && iw.u * SC_BLOCK < iw.len) break;
-            more = iw.next(P, R);
+            more = iw.next(P);
             iw.u = iw.u0 + warp;
         }
         if (more && lane < nb) {  // lane j fetches block j of the tile
@@ -252,9 +258,9 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     };
     for (int s = 0; s < SC_STAGES; ++s) issue();
 
-    Walk w;
+    Walk<SC_BLOCK> w;
     w.begin(P, R);
-    for (bool go = true; go; go = w.next(P, R)) {
+    for (bool go = true; go; go = w.next(P)) {
         const int head = w.hr / P.row_blocks, row0 = (w.hr % P.row_blocks) * SC_ROWS;
         // ---- this segment's queries, in fragment order ----
         uint32_t qa[KS][4];
@@ -632,8 +638,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
             }
         }
         if (tid == 0 && w.u0 == 0 && !whole) {
-            const long long last = (w.start + w.units - 1) / R.chunk;
-            P.desc[blockIdx.x] = make_int4(w.b, w.hr, static_cast<int>(last - blockIdx.x + 1), 0);
+            P.desc[blockIdx.x] = make_int4(w.b, w.hr, w.parts(static_cast<int>(R.chunk)), 0);
         }
         __syncthreads();  // the merge buffers are free
     }
