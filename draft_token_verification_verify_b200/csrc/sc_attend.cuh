@@ -28,7 +28,6 @@ namespace sv {
 constexpr int SC_WARPS = 4;
 constexpr int SC_NT = SC_WARPS * 32;
 constexpr int SC_ROWS = 16;   // rows of a block
-constexpr int SC_STAGES = 2;  // tiles in flight for each warp
 constexpr int SC_MIN_TILES = 4;  // tiles of a CTA's range at least
 
 struct AttendParams {
@@ -84,6 +83,7 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) 
     const int per = (P.B + NT - 1) / NT;
     const long long segs = static_cast<long long>(P.c.kv_heads) * P.row_blocks;
     long long mine = 0;
+#pragma unroll 1
     for (int b = tid * per; b < (tid + 1) * per && b < P.B; ++b) mine += sc_units<TILE>(P, b);
     long long incl = mine;
 #pragma unroll
@@ -101,13 +101,15 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) 
     }
     Range r;
     r.total = total * segs;
-    r.chunk = (r.total + gridDim.x - 1) / gridDim.x;
+    // (rounded up, or one more: a double's error never makes the ranges too short)
+    r.chunk = static_cast<long long>(static_cast<double>(r.total) / gridDim.x) + 1;
     if (r.chunk < min_units) r.chunk = min_units;
     r.g0 = r.chunk * blockIdx.x;
     r.g1 = r.g0 + r.chunk < r.total ? r.g0 + r.chunk : r.total;
     long long at = (base + incl - mine) * segs;
     if (r.g0 < r.g1 && r.g0 >= at && r.g0 < at + mine * segs) {
         int b = tid * per;
+#pragma unroll 1
         for (;; ++b) {
             const long long u = sc_units<TILE>(P, b) * segs;
             if (r.g0 < at + u) break;
@@ -133,17 +135,21 @@ struct Walk {
     int u;           // for the caller: the unit it is at
     bool bad;        // a length above the capacity
 
+    // (the broadcasts tell the compiler that a warp walks as one)
     __device__ __forceinline__ void sequence(const AttendParams& P) {
-        units = sc_units<TILE>(P, b);
-        len = sc_len(P, b, &bad);
+        bool above;
+        len = __shfl_sync(0xffffffffu, sc_len(P, b, &above), 0);
+        bad = __any_sync(0xffffffffu, above);
+        units = (len + TILE - 1) / TILE + sc_new_units<TILE>(P);
+        if (units == 0) units = 1;
     }
     __device__ __forceinline__ void begin(const AttendParams& P, const Range& r) {
-        b = r.b;
+        b = __shfl_sync(0xffffffffu, r.b, 0);
         sequence(P);
         const long long in = r.g0 - r.before;
-        hr = static_cast<int>(in / units);
-        u0 = static_cast<int>(in - static_cast<long long>(hr) * units);
-        left = static_cast<int>(r.g1 - r.g0);
+        hr = __shfl_sync(0xffffffffu, static_cast<int>(static_cast<double>(in) / units), 0);  // exact below 2^53
+        u0 = __shfl_sync(0xffffffffu, static_cast<int>(in - static_cast<long long>(hr) * units), 0);
+        left = __shfl_sync(0xffffffffu, static_cast<int>(r.g1 - r.g0), 0);
         u1 = units - u0 < left ? units : u0 + left;
         left -= u1 - u0;
     }
@@ -172,64 +178,80 @@ __device__ __forceinline__ size_t sc_out_row(const AttendParams& P, int b, int h
     return (static_cast<size_t>(b) * P.n + node) * P.q_heads + head * P.group + g;
 }
 
-template <int D>
+template <int D, int MB>
 struct AttendSmem {
-    // Blocks of a tile lie `stride` bytes apart: shorter blocks are padded so
+    static constexpr int GROUPS = SC_WARPS / MB;  // warps of a group share its tiles, 16 rows each
+    static constexpr int STAGES = MB == 1 ? 2 : MB == 2 ? 4 : 8;
+    static constexpr int ROWS = SC_ROWS * MB;     // of the CTA
+    // Blocks of a tile lie `bstride` bytes apart: shorter blocks are padded so
     // that the four quarter-tiles of a value read fall into different banks.
     static constexpr int TILE = 2 * sc_half_bytes<D>(SC_BLOCK) + 128;
-    static constexpr int RING = SC_WARPS * SC_STAGES * TILE;
+    static constexpr int RING = GROUPS * STAGES * TILE;
     static constexpr int MERGE_ROW = D + 4;  // floats
     static constexpr int MERGE = SC_ROWS * MERGE_ROW * 4;  // a warp's output, or its staged value rows
-    static constexpr int ML = SC_WARPS * SC_ROWS * 8;
-    static constexpr int BYTES = RING + SC_WARPS * MERGE + ML + SC_WARPS * SC_STAGES * 8 + 64;
+    static constexpr int OFF_ML = RING + SC_WARPS * MERGE;
+    static constexpr int OFF_BAD = OFF_ML + SC_WARPS * SC_ROWS * 8;  // int [GROUPS][STAGES]
+    static constexpr int OFF_BAR = OFF_BAD + GROUPS * STAGES * 4;
+    static constexpr int BYTES = OFF_BAR + 2 * GROUPS * STAGES * 8;
     static_assert(SC_ROWS * (D + 8) * 2 <= MERGE, "staged value rows fit the merge buffer");
+    static_assert(OFF_BAR % 8 == 0 && 2 * (BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
-template <int DT, int D>
+template <int DT, int D, int MB>
 __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_constant__ AttendParams P) {
     using Ty = SC<DT>;
-    using Sm = AttendSmem<D>;
+    using Sm = AttendSmem<D, MB>;
     using T = typename Ty::T;
+    constexpr unsigned ALL = 0xffffffffu;
+    constexpr int G = Sm::GROUPS, STAGES = Sm::STAGES;
     constexpr int KS = D / 16;   // k-steps of a dot product
     constexpr int KW = D / 32;   // 32-bit words of a lane's share of a key row
     constexpr int NV = D / 8;    // n-tiles of the output
     extern __shared__ __align__(128) unsigned char sc_raw[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the broadcast tells the compiler that a warp works as one)
+    const int tid = threadIdx.x, warp = __shfl_sync(ALL, tid >> 5, 0), lane = tid & 31;
     const int r8 = lane >> 2, q4 = lane & 3;
-    unsigned char* ring = sc_raw + warp * SC_STAGES * Sm::TILE;
+    const int group = warp / MB, mb = warp % MB;
+    unsigned char* ring = sc_raw + group * STAGES * Sm::TILE;
     float* merge = reinterpret_cast<float*>(sc_raw + Sm::RING + warp * Sm::MERGE);
-    float2* ml = reinterpret_cast<float2*>(sc_raw + Sm::RING + SC_WARPS * Sm::MERGE);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sc_raw + Sm::RING + SC_WARPS * Sm::MERGE + Sm::ML) +
-                     warp * SC_STAGES;
+    float2* ml = reinterpret_cast<float2*>(sc_raw + Sm::OFF_ML);
+    volatile int* bad_s = reinterpret_cast<int*>(sc_raw + Sm::OFF_BAD) + group * STAGES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sc_raw + Sm::OFF_BAR) + group * STAGES;
+    uint64_t* empty = full + G * STAGES;  // (MB > 1: the group's warps have read a stage)
     const CacheView& c = P.c;
+    const float nan = __int_as_float(0x7fffffff);
 
     pdl_launch_dependents();
     const Range R = sc_range<SC_NT, SC_BLOCK>(P, SC_MIN_TILES);
-    int error = 0;
+    bool error = false;
     if (tid == 0) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (R.g0 >= R.g1) return;
-    if (lane == 0) {
-        for (int s = 0; s < SC_STAGES; ++s) mbar_init(&bars[s], 1);
+    if (mb == 0 && lane == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], MB);
+        }
         fence_mbar_init();
     }
-    __syncwarp();
+    __syncthreads();
 
     const int nb = SC_BLOCK >> c.log2_block;  // blocks of a tile
-    const int bstride = 2 * sc_half_bytes<D>(c.block) + (nb == 1 ? 0 : nb == 2 ? 64 : 32);
+    const uint32_t bbytes = 2 * sc_half_bytes<D>(c.block);
+    const uint32_t bstride = bbytes + (nb == 1 ? 0 : nb == 2 ? 64 : 32);
     const float sl = P.scale * SC_LOG2E;
 
-    // ---- the copies: tile `iw` of this warp is issued SC_STAGES tiles ahead ----
+    // ---- the copies of a group, by its first warp: STAGES tiles ahead ----
     Walk<SC_BLOCK> iw;
     iw.begin(P, R);
-    iw.u = iw.u0 + warp;
+    iw.u = iw.u0 + group;
     bool more = true;
     int ahead_id = 0, ahead_sub = 0;
-    uint32_t bad_stage = 0;  // bit s: a page of stage s was out of range
-    auto settle = [&]() {    // to the next cache tile at or behind iw.u
+    auto settle = [&]() {  // to the next cache tile at or behind iw.u
+#pragma unroll 1
         while (more) {
             if (iw.u < iw.u1 && iw.u * SC_BLOCK < iw.len) break;
             more = iw.next(P);
-            iw.u = iw.u0 + warp;
+            iw.u = iw.u0 + group;
         }
         if (more && lane < nb) {  // lane j fetches block j of the tile
             const int t = iw.u * SC_BLOCK + (lane << c.log2_block);
@@ -237,31 +259,54 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
             ahead_sub = (t & (c.page_size - 1)) >> c.log2_block;
         }
     };
-    settle();
     int issued = 0, used = 0;
     auto issue = [&]() {
-        if (!more) return;
-        const int s = issued % SC_STAGES;
-        const int head = iw.hr / P.row_blocks;
-        const uint32_t bytes = 2 * sc_half_bytes<D>(c.block);
+        if (!more || error) return;
+        const int s = issued % STAGES;
+        if (MB > 1 && issued >= STAGES && !sc_wait(&empty[s], ((issued / STAGES) - 1) & 1, P.timeout_ns)) {
+            error = true;
+            return;
+        }
         const bool mine = lane < nb && ahead_id != -2;
         const bool ok = mine && ahead_id >= 0 && ahead_id < c.num_pages && !P.test_hook;
-        const unsigned got = __ballot_sync(0xffffffffu, ok);
-        const unsigned want = __ballot_sync(0xffffffffu, mine);
-        bad_stage = (bad_stage & ~(1u << s)) | ((got != want && !P.test_hook) ? 1u << s : 0u);
-        if (lane == 0) mbar_arrive_expect_tx(&bars[s], P.test_hook ? bytes : bytes * __popc(got));
+        const unsigned got = __ballot_sync(ALL, ok), want = __ballot_sync(ALL, mine);
+        if (lane == 0) {
+            bad_s[s] = got != want && !P.test_hook;
+            mbar_arrive_expect_tx(&full[s], P.test_hook ? bbytes : bbytes * __popc(got));
+        }
         __syncwarp();
-        if (ok) bulk_g2s(ring + s * Sm::TILE + lane * bstride, sc_block_ptr<D>(c, ahead_id, head, ahead_sub), bytes, &bars[s]);
+        if (ok)
+            bulk_g2s(ring + s * Sm::TILE + lane * bstride, sc_block_ptr<D>(c, ahead_id, iw.hr / P.row_blocks, ahead_sub),
+                     bbytes, &full[s]);
         ++issued;
-        iw.u += SC_WARPS;
+        iw.u += G;
         settle();
     };
-    for (int s = 0; s < SC_STAGES; ++s) issue();
+    if (mb == 0) {
+        settle();
+#pragma unroll 1
+        for (int s = 0; s < (MB == 1 ? STAGES : STAGES - 1); ++s) issue();
+    }
+
+    // Token 2 t + i of a lane's 16: what its code's product and its weight are
+    // multiplied by (even and odd t).
+    const float k_code = DT == 0 ? SC_2P69 : 16777216.f;
+    const uint64_t v_even = DT == 0 ? f2_pack(SC_2P64, SC_2P64) : f2_pack(1.f, 1.f);
+    const uint64_t v_odd = DT == 0 ? f2_pack(SC_2P60, SC_2P60) : v_even;
+    const uint64_t kc2 = f2_pack(sl * k_code, sl * k_code), sl2 = f2_pack(sl, sl), eight2 = f2_pack(8.f, 8.f);
+    // this lane's shares of a tile: its key rows, its 16 tokens' parameters, its value rows
+    const int tk = 16 * (r8 >> 1), tq = 16 * q4, Tb = c.block;
+    const uint32_t k_off = (tk >> c.log2_block) * bstride + ((tk & (Tb - 1)) + (r8 & 1)) * (D / 2) + q4 * (D / 8);
+    const uint32_t q_blk = (tq >> c.log2_block) * bstride;
+    const uint32_t p_off = q_blk + Tb * (D / 2) + (tq & (Tb - 1)) * 4;
+    const uint32_t v_off = q_blk + sc_half_bytes<D>(Tb) + r8 * (Tb / 2) + (tq & (Tb - 1)) / 2;
+    const uint32_t half_bytes = sc_half_bytes<D>(Tb), v_step = 8 * (Tb / 2);
 
     Walk<SC_BLOCK> w;
     w.begin(P, R);
+#pragma unroll 1
     for (bool go = true; go; go = w.next(P)) {
-        const int head = w.hr / P.row_blocks, row0 = (w.hr % P.row_blocks) * SC_ROWS;
+        const int head = w.hr / P.row_blocks, row0 = (w.hr % P.row_blocks) * Sm::ROWS + mb * SC_ROWS;
         // ---- this segment's queries, in fragment order ----
         uint32_t qa[KS][4];
         float qs[2] = {0.f, 0.f};
@@ -275,188 +320,229 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                            static_cast<long long>(head * P.group + g) * D + q4 * (D / 4);
 #pragma unroll
             for (int i = 0; i < KS / 2; ++i) {
-                const uint4 x = in ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                uint4 x = in ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                qs[e] += (Ty::lo(x.x) + Ty::hi(x.x)) + (Ty::lo(x.y) + Ty::hi(x.y)) + (Ty::lo(x.z) + Ty::hi(x.z)) +
+                         (Ty::lo(x.w) + Ty::hi(x.w));
+                if constexpr (DT == 0) {  // 2^64, and 2^60 where the code is 16-fold (exact)
+                    x.x = Ty::pack(Ty::lo(x.x) * SC_2P64, Ty::hi(x.x) * SC_2P64);
+                    x.y = Ty::pack(Ty::lo(x.y) * SC_2P60, Ty::hi(x.y) * SC_2P60);
+                    x.z = Ty::pack(Ty::lo(x.z) * SC_2P64, Ty::hi(x.z) * SC_2P64);
+                    x.w = Ty::pack(Ty::lo(x.w) * SC_2P60, Ty::hi(x.w) * SC_2P60);
+                }
                 qa[2 * i][e] = x.x;
                 qa[2 * i][2 + e] = x.y;
                 qa[2 * i + 1][e] = x.z;
                 qa[2 * i + 1][2 + e] = x.w;
-                qs[e] += (Ty::lo(x.x) + Ty::hi(x.x)) + (Ty::lo(x.y) + Ty::hi(x.y)) + (Ty::lo(x.z) + Ty::hi(x.z)) +
-                         (Ty::lo(x.w) + Ty::hi(x.w));
             }
-            qs[e] += __shfl_xor_sync(0xffffffffu, qs[e], 1);
-            qs[e] += __shfl_xor_sync(0xffffffffu, qs[e], 2);
+            qs[e] += __shfl_xor_sync(ALL, qs[e], 1);
+            qs[e] += __shfl_xor_sync(ALL, qs[e], 2);
         }
-        float o[NV][4];
+        float o[NV][4], o8[4];  // the output, and 8 of every weight
 #pragma unroll
         for (int u = 0; u < NV; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[u][i] = 0.f;
-        float m[2] = {SC_NEG_INF, SC_NEG_INF}, l[2] = {0.f, 0.f}, z[2] = {0.f, 0.f};
-        if (w.bad) l[0] = l[1] = __int_as_float(0x7fffffff);  // a length above the capacity
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o8[i] = 0.f;
+        // of the rows r8 and r8 + 8: the reference (-inf: none), minus it (0: none), sums over even and odd tokens
+        float m[2] = {SC_NEG_INF, SC_NEG_INF}, nref[2] = {0.f, 0.f};
+        uint64_t l[2] = {0ull, 0ull}, z[2] = {0ull, 0ull};
+        bool unset = true;  // a row of the warp has no reference yet
+        auto poison = [&]() { l[0] = l[1] = f2_pack(nan, nan); };
+        if (w.bad) poison();  // a length above the capacity
 
-        // A new maximum rescales what was summed, but only where it passes the
-        // reference by 2^8: until then the weights just exceed 1.
-        auto reference = [&](float mx, int e) {
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const bool up = mx > m[e] + 8.f;  // also from -inf
-            if (__any_sync(0xffffffffu, up)) {
-                const float f = up ? ex2(m[e] - mx) : 1.f;
-                if (up) m[e] = mx;
-                l[e] *= f;
-                z[e] *= f;
+        // Moves the references that have none, or that a score passed by 2^8 (until
+        // then the weights just exceed 1); `top` are the lane's largest scores
+        // relative to them.  Returns what the scores change by.
+        auto move = [&](const float (&top)[2], float (&by)[2]) {
+            unset = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(top[e], __shfl_xor_sync(ALL, top[e], 1));
+                mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, 2)) - nref[e];
+                float f = 1.f;
+                by[e] = 0.f;
+                if (mx > m[e] + 8.f) {  // also from -inf
+                    f = m[e] == SC_NEG_INF ? 0.f : ex2(m[e] - mx);
+                    by[e] = -mx - nref[e];
+                    m[e] = mx;
+                    nref[e] = -mx;
+                }
+                unset |= m[e] == SC_NEG_INF;
+                const uint64_t f2 = f2_pack(f, f);
+                l[e] = f2_mul(l[e], f2);
+                z[e] = f2_mul(z[e], f2);
+                o8[2 * e] *= f;
+                o8[2 * e + 1] *= f;
 #pragma unroll
                 for (int u = 0; u < NV; ++u) {
                     o[u][2 * e] *= f;
                     o[u][2 * e + 1] *= f;
                 }
             }
-            return m[e] == SC_NEG_INF ? 0.f : m[e];
+            unset = __any_sync(ALL, unset);
         };
 
-        const int first = w.u0 + warp;
-        for (int u = first; u < w.u1; u += SC_WARPS) {
+#pragma unroll 1
+        for (int u = w.u0 + group; u < w.u1; u += G) {
             if (u * SC_BLOCK < w.len) {
                 // ---- a tile of 64 cached tokens ----
-                const int s = used % SC_STAGES;
-                if (!error) {
-                    const bool got = mbar_wait_bounded(&bars[s], (used / SC_STAGES) & 1, P.timeout_ns);
-                    error = !__all_sync(0xffffffffu, got);
-                }
-                if (error || ((bad_stage >> s) & 1u)) l[0] = l[1] = __int_as_float(0x7fffffff);
+                if (MB > 1 && mb == 0) issue();  // into the stage of the tile before this one
+                const int s = used % STAGES;
+                if (!error) error = !sc_wait(&full[s], (used / STAGES) & 1, P.timeout_ns);
+                if (error || __any_sync(ALL, bad_s[s])) poison();
                 if (error) continue;  // nothing more is waited for
                 ++used;
-                const int valid = w.len - u * SC_BLOCK < SC_BLOCK ? w.len - u * SC_BLOCK : SC_BLOCK;
+                const int valid = w.len - u * SC_BLOCK;
                 const unsigned char* tile = ring + s * Sm::TILE;
-                const int Tb = c.block;
+                // scores: lane r8 of n-tile t takes token 16 (r8 / 2) + 2 t + r8 % 2, so that
+                // the accumulators of a lane are the 16 tokens 16 q4 .. 16 q4 + 15
                 float x[8][4];
-                {
-                    // scores: lane r8 of n-tile t takes token 16 (r8 / 2) + 2 t + r8 % 2, so that
-                    // the accumulators of a lane are the 16 tokens 16 q4 .. 16 q4 + 15
-                    const int tk = 16 * (r8 >> 1);
-                    const unsigned char* krow = tile + (tk >> c.log2_block) * bstride +
-                                                ((tk & (Tb - 1)) + (r8 & 1)) * (D / 2) + q4 * (D / 8);
 #pragma unroll
-                    for (int t4 = 0; t4 < 8; t4 += 4) {
-                        uint32_t kw[4][KW];
+                for (int t4 = 0; t4 < 8; t4 += 4) {
+                    uint32_t kw[4][KW];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const unsigned char* a = tile + k_off + (t4 + i) * D;
+                        if constexpr (KW == 4) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(a);
+                            kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(a);
+                            kw[i][0] = v.x, kw[i][1] = v.y;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[t4 + i][j] = 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < KS; k += 2)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const unsigned char* a = krow + (t4 + i) * D;
-                            if constexpr (KW == 4) {
-                                const uint4 v = *reinterpret_cast<const uint4*>(a);
-                                kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
-                            } else {
-                                const uint2 v = *reinterpret_cast<const uint2*>(a);
-                                kw[i][0] = v.x, kw[i][1] = v.y;
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) x[t4 + i][j] = 0.f;
+                            const uint32_t wd = kw[i][k >> 1], w8 = wd >> 8;
+                            sc_mma<DT>(x[t4 + i], qa[k], sc_codes<DT == 0>(wd, w8, 0), sc_codes<DT == 0>(wd, w8, 1));
+                            sc_mma<DT>(x[t4 + i], qa[k + 1], sc_codes<DT == 0>(wd, w8, 2), sc_codes<DT == 0>(wd, w8, 3));
                         }
+                }
+                // relative to the reference: scale (q . code) + zero sum(q) - reference
+                const uint64_t q2[2] = {f2_pack(qs[0], qs[0]), f2_pack(qs[1], qs[1])};
+                const uint64_t n2[2] = {f2_pack(nref[0], nref[0]), f2_pack(nref[1], nref[1])};
 #pragma unroll
-                        for (int k = 0; k < KS; ++k)
+                for (int t = 0; t < 8; t += 2) {
+                    const uint4 pr = *reinterpret_cast<const uint4*>(tile + p_off + t * 8);
+                    const uint32_t pw[4] = {pr.x, pr.y, pr.z, pr.w};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t wd = kw[i][k >> 1];
-                                if constexpr (DT == 0)
-                                    sc_mma<0>(x[t4 + i], qa[k], sc_codes_bf16(wd, 2 * (k & 1)),
-                                              sc_codes_bf16(wd, 2 * (k & 1) + 1));
-                                else
-                                    sc_mma<1>(x[t4 + i], qa[k], sc_center_f16(sc_codes_f16(wd, 2 * (k & 1))),
-                                              sc_center_f16(sc_codes_f16(wd, 2 * (k & 1) + 1)));
-                            }
-                    }
-                    const int tq = 16 * q4;
-                    const unsigned char* kblk = tile + (tq >> c.log2_block) * bstride;
-                    const unsigned char* par = kblk + Tb * (D / 2) + (tq & (Tb - 1)) * 4;
-                    float mx[2] = {SC_NEG_INF, SC_NEG_INF};
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t a2 = f2_mul(f2_pack(Ty::lo(pw[2 * h]), Ty::lo(pw[2 * h + 1])), kc2);
+                        const uint64_t b2 = f2_mul(f2_pack(Ty::hi(pw[2 * h]), Ty::hi(pw[2 * h + 1])), sl2);
 #pragma unroll
-                    for (int t = 0; t < 8; t += 2) {
-                        const uint4 pr = *reinterpret_cast<const uint4*>(par + t * 8);
-                        const uint32_t pw[4] = {pr.x, pr.y, pr.z, pr.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float s1 = Ty::lo(pw[i]);
-                            const float f = s1 * sl;
-                            // codes enter as 128 + code (bf16) or code - 8 (fp16)
-                            const float zz = fmaf(DT == 0 ? -128.f : 8.f, s1, Ty::hi(pw[i])) * sl;
-                            float* a = x[t + (i >> 1)];
-                            a[i & 1] = fmaf(f, a[i & 1], zz * qs[0]);
-                            a[2 + (i & 1)] = fmaf(f, a[2 + (i & 1)], zz * qs[1]);
+                        for (int e = 0; e < 2; ++e) {
+                            float* d = &x[t + h][2 * e];
+                            f2_unpack(f2_fma(a2, f2_pack(d[0], d[1]), f2_fma(b2, q2[e], n2[e])), d[0], d[1]);
                         }
-                    }
-                    if (valid < SC_BLOCK) {
-#pragma unroll
-                        for (int t = 0; t < 8; ++t)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                if (tq + 2 * t + i >= valid) x[t][i] = x[t][2 + i] = SC_NEG_INF;
-                    }
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        mx[0] = fmaxf(mx[0], fmaxf(x[t][0], x[t][1]));
-                        mx[1] = fmaxf(mx[1], fmaxf(x[t][2], x[t][3]));
-                    }
-                    const float m0 = reference(mx[0], 0), m1 = reference(mx[1], 1);
-                    // softmax weights times the values' scales
-                    const unsigned char* vblk = kblk + sc_half_bytes<D>(Tb);
-                    const unsigned char* vpar = vblk + Tb * (D / 2) + (tq & (Tb - 1)) * 4;
-                    uint32_t pa[4][4];
-#pragma unroll
-                    for (int t = 0; t < 8; t += 2) {
-                        const uint4 pr = *reinterpret_cast<const uint4*>(vpar + t * 8);
-                        const uint32_t pw[4] = {pr.x, pr.y, pr.z, pr.w};
-#pragma unroll
-                        for (int h2 = 0; h2 < 2; ++h2) {
-                            float ps[2][2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t pp = pw[2 * h2 + i];
-                                float s1 = Ty::lo(pp), z1 = fmaf(8.f, s1, Ty::hi(pp));
-                                if (valid < SC_BLOCK && tq + 2 * (t + h2) + i >= valid) s1 = z1 = 0.f;
-                                const float p0 = ex2(x[t + h2][i] - m0), p1 = ex2(x[t + h2][2 + i] - m1);
-                                l[0] += p0;
-                                l[1] += p1;
-                                z[0] = fmaf(p0, z1, z[0]);
-                                z[1] = fmaf(p1, z1, z[1]);
-                                ps[0][i] = p0 * s1;
-                                ps[1][i] = p1 * s1;
-                            }
-                            // rounded to bf16 whatever the cache's type: p * scale keeps fp32's range there
-                            pa[t >> 1][2 * h2] = SC<0>::pack(ps[0][0], ps[0][1]);
-                            pa[t >> 1][2 * h2 + 1] = SC<0>::pack(ps[1][0], ps[1][1]);
-                        }
-                    }
-                    const unsigned char* vrow = vblk + r8 * (Tb / 2) + (tq & (Tb - 1)) / 2;
-#pragma unroll
-                    for (int u4 = 0; u4 < NV; u4 += 4) {
-                        uint2 vw[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            vw[i] = *reinterpret_cast<const uint2*>(vrow + (u4 + i) * 8 * (Tb / 2));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t wd = k < 2 ? vw[i].x : vw[i].y;
-                                sc_mma<0>(o[u4 + i], pa[k], sc_center_bf16(sc_codes_bf16(wd, 2 * (k & 1))),
-                                          sc_center_bf16(sc_codes_bf16(wd, 2 * (k & 1) + 1)));
-                            }
                     }
                 }
+                if (valid < SC_BLOCK) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (tq + 2 * t + i >= valid) x[t][i] = x[t][2 + i] = SC_NEG_INF;
+                }
+                float top[2] = {SC_NEG_INF, SC_NEG_INF};
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    top[0] = fmaxf(top[0], fmaxf(x[t][0], x[t][1]));
+                    top[1] = fmaxf(top[1], fmaxf(x[t][2], x[t][3]));
+                }
+                if (unset || __any_sync(ALL, fmaxf(top[0], top[1]) > 8.f)) {
+                    float by[2];
+                    move(top, by);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[t][i] += by[i >> 1];
+                }
+                // softmax weights times the values' scales
+                uint32_t pa[4][4], pl[4][4];
+#pragma unroll
+                for (int t = 0; t < 8; t += 2) {
+                    const uint4 pr = *reinterpret_cast<const uint4*>(tile + p_off + half_bytes + t * 8);
+                    uint32_t pw[4] = {pr.x, pr.y, pr.z, pr.w};
+                    if (valid < SC_BLOCK) {  // what lies behind the last token may be anything
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (tq + 2 * t + i >= valid) pw[i] = 0u;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t s2 = f2_pack(Ty::lo(pw[2 * h]), Ty::lo(pw[2 * h + 1]));
+                        // the values' middle: codes count from 8
+                        const uint64_t z2 = f2_fma(s2, eight2, f2_pack(Ty::hi(pw[2 * h]), Ty::hi(pw[2 * h + 1])));
+                        const uint64_t sv2 = DT == 0 ? f2_mul(s2, h ? v_odd : v_even) : s2;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint64_t p2 = f2_pack(ex2(x[t + h][2 * e]), ex2(x[t + h][2 * e + 1]));
+                            l[e] = f2_add(l[e], p2);
+                            z[e] = f2_fma(p2, z2, z[e]);
+                            float s0, s1;
+                            f2_unpack(f2_mul(p2, sv2), s0, s1);
+                            // rounded to bf16 whatever the cache's type: p * scale keeps fp32's range there;
+                            // with fp16 activations the rest goes through the product as well
+                            const uint32_t hi = SC<0>::pack(s0, s1);
+                            pa[t >> 1][2 * h + e] = hi;
+                            if constexpr (DT == 1) pl[t >> 1][2 * h + e] = SC<0>::pack(s0 - SC<0>::lo(hi), s1 - SC<0>::hi(hi));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u4 = 0; u4 < NV; u4 += 4) {
+                    uint2 vw[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        vw[i] = *reinterpret_cast<const uint2*>(tile + v_off + (u4 + i) * v_step);
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t wd = k ? vw[i].y : vw[i].x, w8 = wd >> 8;
+                            uint32_t vb[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                vb[j] = DT == 0 ? sc_codes<true>(wd, w8, j) : sc_center_bf16(sc_codes_bf16(wd, j));
+                            sc_mma<0>(o[u4 + i], pa[k], vb[0], vb[1]);
+                            sc_mma<0>(o[u4 + i], pa[k + 1], vb[2], vb[3]);
+                            if constexpr (DT == 1) {
+                                sc_mma<0>(o[u4 + i], pl[k], vb[0], vb[1]);
+                                sc_mma<0>(o[u4 + i], pl[k + 1], vb[2], vb[3]);
+                            }
+                        }
+                }
+                // bf16 codes count from 0 in the product: 8 of the rounded weights are summed beside
+                // it, so that a weight's rounding meets code - 8 in the end and not code
+                if constexpr (DT == 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc_mma<0>(o8, pa[k], 0x00080008u, 0x00800080u);
+                }
                 __syncwarp();
-                issue();  // into the stage just read
+                if constexpr (MB == 1) {
+                    issue();  // into the stage just read
+                } else {
+                    if (lane == 0) sc_arrive(&empty[s]);
+                }
             } else if (P.k_new) {
                 // ---- up to 64 of the scored positions, 16 at a time ----
                 const int ub = (u - (w.len + SC_BLOCK - 1) / SC_BLOCK) * SC_BLOCK;
                 const int32_t* par = P.parents ? P.parents + static_cast<size_t>(w.b) * (P.n - 1) : nullptr;
                 if (par) {
                     int bad = 0;
+#pragma unroll 1
                     for (int i = 1 + lane; i < P.n; i += 32) bad |= par[i - 1] < 0 || par[i - 1] >= i;
-                    if (__any_sync(0xffffffffu, bad)) {  // no such tree
-                        l[0] = l[1] = __int_as_float(0x7fffffff);
+                    if (__any_sync(ALL, bad)) {  // no such tree
+                        poison();
                         continue;
                     }
                 }
+#pragma unroll 1
                 for (int j0 = ub; j0 < ub + SC_BLOCK && j0 < P.n; j0 += 16) {
                     float x[2][4];
                     const long long tok = static_cast<long long>(w.b) * P.n;
@@ -470,7 +556,11 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                         for (int i = 0; i < 4; ++i) x[t][i] = 0.f;
 #pragma unroll
                         for (int i = 0; i < KS / 2; ++i) {
-                            const uint4 kx = in ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                            uint4 kx = in ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                            if constexpr (DT == 0) {  // against the queries' 2^60
+                                kx.y = Ty::pack(Ty::lo(kx.y) * 16.f, Ty::hi(kx.y) * 16.f);
+                                kx.w = Ty::pack(Ty::lo(kx.w) * 16.f, Ty::hi(kx.w) * 16.f);
+                            }
                             sc_mma<DT>(x[t], qa[2 * i], kx.x, kx.y);
                             sc_mma<DT>(x[t], qa[2 * i + 1], kx.z, kx.w);
                         }
@@ -481,6 +571,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                     T* vs = reinterpret_cast<T*>(merge);
                     uint32_t odd = 0;
                     __syncwarp();
+#pragma unroll 1
                     for (int i = lane; i < 16 * (D / 8); i += 32) {
                         const int jr = i / (D / 8), dc = i % (D / 8);
                         uint4 vx = make_uint4(0u, 0u, 0u, 0u);
@@ -496,48 +587,67 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                         if (!fine) odd |= 1u << jr;
                         *reinterpret_cast<uint4*>(vs + jr * (D + 8) + dc * 8) = vx;
                     }
-                    odd = __reduce_or_sync(0xffffffffu, odd);
+                    odd = __reduce_or_sync(ALL, odd);
                     if (odd) {
+#pragma unroll 1
                         for (int i = lane; i < 16 * (D / 8); i += 32)
                             if ((odd >> (i / (D / 8))) & 1u)
                                 *reinterpret_cast<uint4*>(vs + (i / (D / 8)) * (D + 8) + (i % (D / 8)) * 8) =
                                     make_uint4(0u, 0u, 0u, 0u);
                     }
                     __syncwarp();
-                    float mx[2] = {SC_NEG_INF, SC_NEG_INF};
+                    float top[2] = {SC_NEG_INF, SC_NEG_INF};
+                    const float kn = DT == 0 ? sl / SC_2P64 : sl;
                     uint32_t seen = 0;  // bit 4 e + 2 t + i: row e sees position 8 t + 2 q4 + i
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int row = row0 + r8 + 8 * e;
                         const int node = row / P.group;
+                        if (row < P.rows) {
+                            if (par) {  // the node's path, down to these positions
+                                int a = node;
+#pragma unroll 1
+                                while (a >= j0) {
+                                    const int i = a - j0;
+                                    if (i < 16 && ((i & 7) >> 1) == q4) seen |= 1u << (4 * e + 2 * (i >> 3) + (i & 1));
+                                    a = a > 0 ? par[a - 1] : -1;
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (j0 + 8 * (i >> 1) + 2 * q4 + (i & 1) <= node) seen |= 1u << (4 * e + i);
+                            }
+                        }
 #pragma unroll
                         for (int t = 0; t < 2; ++t)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const int j = j0 + 8 * t + 2 * q4 + i;
-                                bool see = row < P.rows && j < P.n && j <= node;
-                                if (see && par) {  // climb from the node to the position, or past it
-                                    int a = node;
-                                    while (a > j) a = par[a - 1];
-                                    see = a == j;
-                                }
-                                seen |= see ? 1u << (4 * e + 2 * t + i) : 0u;
-                                x[t][2 * e + i] = see ? x[t][2 * e + i] * sl : SC_NEG_INF;
-                                mx[e] = fmaxf(mx[e], x[t][2 * e + i]);
+                                const bool see = (seen >> (4 * e + 2 * t + i)) & 1u;
+                                x[t][2 * e + i] = see ? fmaf(x[t][2 * e + i], kn, nref[e]) : SC_NEG_INF;
+                                top[e] = fmaxf(top[e], x[t][2 * e + i]);
                             }
                     }
-                    const float mm[2] = {reference(mx[0], 0), reference(mx[1], 1)};
+                    __syncwarp();
+                    if (unset || __any_sync(ALL, fmaxf(top[0], top[1]) > 8.f)) {
+                        float by[2];
+                        move(top, by);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[t][i] += by[i >> 1];
+                    }
                     float p[2][4];
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int e = i >> 1;
-                            p[t][i] = (seen >> (4 * e + 2 * t + (i & 1))) & 1u ? ex2(x[t][i] - mm[e]) : 0.f;
-                            l[e] += p[t][i];
-                        }
-                    const uint32_t pa[4] = {Ty::pack(p[0][0], p[0][1]), Ty::pack(p[0][2], p[0][3]),
-                                            Ty::pack(p[1][0], p[1][1]), Ty::pack(p[1][2], p[1][3])};
+                        for (int i = 0; i < 4; ++i)
+                            p[t][i] = (seen >> (4 * (i >> 1) + 2 * t + (i & 1))) & 1u ? ex2(x[t][i]) : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        l[e] = f2_add(l[e], f2_pack(p[0][2 * e] + p[1][2 * e], p[0][2 * e + 1] + p[1][2 * e + 1]));
+                    const float pv = DT == 0 ? 1.f / SC_2P69 : 1.f;  // the output's scale
+                    const uint32_t pa[4] = {Ty::pack(p[0][0] * pv, p[0][1] * pv), Ty::pack(p[0][2] * pv, p[0][3] * pv),
+                                            Ty::pack(p[1][0] * pv, p[1][1] * pv), Ty::pack(p[1][2] * pv, p[1][3] * pv)};
 #pragma unroll
                     for (int v = 0; v < NV; v += 2) {
                         uint32_t b4[4];
@@ -548,6 +658,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                         sc_mma<DT>(o[v], pa, b4[0], b4[1]);
                         sc_mma<DT>(o[v + 1], pa, b4[2], b4[3]);
                     }
+#pragma unroll 1
                     for (; odd; odd &= odd - 1) {
                         const int jr = __ffs(odd) - 1;
                         const T* src = static_cast<const T*>(P.v_new) + (tok + j0 + jr) * P.kv_stride +
@@ -558,8 +669,8 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                             const int bit = 4 * e + 2 * (jr >> 3) + (jr & 1);
                             const float mine = (jr >> 3) ? ((jr & 1) ? p[1][2 * e + 1] : p[1][2 * e])
                                                          : ((jr & 1) ? p[0][2 * e + 1] : p[0][2 * e]);
-                            const float pe = __shfl_sync(0xffffffffu, mine, from);
-                            const bool see = (__shfl_sync(0xffffffffu, seen, from) >> bit) & 1u;
+                            const float pe = __shfl_sync(ALL, mine, from) * pv;
+                            const bool see = (__shfl_sync(ALL, seen, from) >> bit) & 1u;
 #pragma unroll
                             for (int u8 = 0; u8 < NV; ++u8) {
                                 const uint32_t vv = *reinterpret_cast<const uint32_t*>(src + u8 * 8 + 2 * q4);
@@ -575,77 +686,83 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
             }
         }
 
-        // ---- merge the warps: 16 rows of (max, sum, output) ----
+        // ---- merge the groups: 16 rows of (reference, sum, output) a warp ----
+        const float os = DT == 0 ? SC_2P69 : 1.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-            z[e] += __shfl_xor_sync(0xffffffffu, z[e], 1);
-            z[e] += __shfl_xor_sync(0xffffffffu, z[e], 2);
+            float a, b;
+            f2_unpack(l[e], a, b);
+            float ls = a + b;
+            f2_unpack(z[e], a, b);
+            float zs = a + b;
+            ls += __shfl_xor_sync(ALL, ls, 1);
+            ls += __shfl_xor_sync(ALL, ls, 2);
+            zs += __shfl_xor_sync(ALL, zs, 1);
+            zs += __shfl_xor_sync(ALL, zs, 2);
             const int r = r8 + 8 * e;
-            if (q4 == 0) ml[warp * SC_ROWS + r] = make_float2(m[e], l[e]);
+            if (q4 == 0) ml[warp * SC_ROWS + r] = make_float2(m[e], ls);
 #pragma unroll
             for (int u = 0; u < NV; ++u)
                 *reinterpret_cast<float2*>(merge + r * Sm::MERGE_ROW + u * 8 + 2 * q4) =
-                    make_float2(o[u][2 * e] + z[e], o[u][2 * e + 1] + z[e]);
+                    make_float2(fmaf(o[u][2 * e] - o8[2 * e], os, zs), fmaf(o[u][2 * e + 1] - o8[2 * e], os, zs));
         }
         __syncthreads();
         const bool whole = w.whole();
         const int slot = blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0);
         const float* all = reinterpret_cast<const float*>(sc_raw + Sm::RING);
-        constexpr int PER = SC_NT / SC_ROWS;  // threads of a row
+        constexpr int PER = SC_NT / Sm::ROWS;  // threads of a row
         const int r = tid / PER, cpart = tid % PER;
-        float M = SC_NEG_INF, L = 0.f, wt[SC_WARPS];
+        const int first = (r / SC_ROWS), r16 = r % SC_ROWS;  // warps first, first + MB, ... hold the row
+        float M = SC_NEG_INF, L = 0.f, wt[G];
 #pragma unroll
-        for (int i = 0; i < SC_WARPS; ++i) M = fmaxf(M, ml[i * SC_ROWS + r].x);
+        for (int i = 0; i < G; ++i) M = fmaxf(M, ml[(first + i * MB) * SC_ROWS + r16].x);
 #pragma unroll
-        for (int i = 0; i < SC_WARPS; ++i) {
-            const float2 v = ml[i * SC_ROWS + r];
+        for (int i = 0; i < G; ++i) {
+            const float2 v = ml[(first + i * MB) * SC_ROWS + r16];
             wt[i] = v.x == SC_NEG_INF ? 0.f : ex2(v.x - M);
-            L += v.x == SC_NEG_INF ? v.y : v.y * wt[i];  // (without a maximum the sum is 0 or NaN)
+            L += v.x == SC_NEG_INF ? v.y : v.y * wt[i];  // (without a reference the sum is 0 or NaN)
         }
-        const int row = row0 + r;
-        const float norm = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        const int row = (w.hr % P.row_blocks) * Sm::ROWS + r;
+        const float norm = L != L ? nan : !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
         if (row < P.rows || !whole) {
             const size_t orow = whole ? sc_out_row(P, w.b, head, row) : 0;
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < D / (4 * PER); ++i) {
                 const int d = (i * PER + cpart) * 4;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < SC_WARPS; ++k) {
-                    const float4 v = *reinterpret_cast<const float4*>(all + k * (Sm::MERGE / 4) + r * Sm::MERGE_ROW + d);
+                for (int k = 0; k < G; ++k) {
+                    const float4 v = *reinterpret_cast<const float4*>(all + (first + k * MB) * (Sm::MERGE / 4) +
+                                                                      r16 * Sm::MERGE_ROW + d);
                     a.x = fmaf(wt[k], v.x, a.x);
                     a.y = fmaf(wt[k], v.y, a.y);
                     a.z = fmaf(wt[k], v.z, a.z);
                     a.w = fmaf(wt[k], v.w, a.w);
                 }
+                a.x *= norm, a.y *= norm, a.z *= norm, a.w *= norm;
                 if (whole) {
-                    uint2 y;
-                    y.x = Ty::pack(a.x * norm, a.y * norm);
-                    y.y = Ty::pack(a.z * norm, a.w * norm);
-                    if (L != L) y = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+                    const uint2 y = make_uint2(Ty::pack(a.x, a.y), Ty::pack(a.z, a.w));
                     *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + orow * D + d) = y;
                 } else {
-                    *reinterpret_cast<float4*>(P.part_o + (static_cast<size_t>(slot) * SC_ROWS + r) * D + d) = a;
+                    *reinterpret_cast<float4*>(P.part_o + (static_cast<size_t>(slot) * Sm::ROWS + r) * D + d) = a;
                 }
             }
             if (cpart == 0) {
                 if (!whole)
-                    P.part_ml[static_cast<size_t>(slot) * SC_ROWS + r] = make_float2(M, L);
+                    P.part_ml[static_cast<size_t>(slot) * Sm::ROWS + r] = make_float2(M, L);
                 else if (P.out_lse)
                     P.out_lse[orow] = L == 0.f ? SC_NEG_INF : (M + log2f(L)) * SC_LN2;
             }
         }
-        if (tid == 0 && w.u0 == 0 && !whole) {
+        if (tid == 0 && w.u0 == 0 && !whole)
             P.desc[blockIdx.x] = make_int4(w.b, w.hr, w.parts(static_cast<int>(R.chunk)), 0);
-        }
         __syncthreads();  // the merge buffers are free
     }
     // no copy may land after the CTA is gone (after an error some are still under way)
-    while (used < issued) {
-        if (!mbar_wait_bounded(&bars[used % SC_STAGES], (used / SC_STAGES) & 1, P.timeout_ns)) error = 1;
-        ++used;
+    if (mb == 0) {
+#pragma unroll 1
+        for (; used < issued; ++used)
+            if (!sc_wait(&full[used % STAGES], (used / STAGES) & 1, P.timeout_ns)) error = true;
     }
     if (error && lane == 0) P.desc[blockIdx.x].w = 1;
 }

@@ -7,18 +7,28 @@
 namespace sv {
 
 namespace {
+template <int DT, int D, int MB>
+AttendKernel warps() {
+    return {sc_attend_kernel<DT, D, MB>, SC_NT, AttendSmem<D, MB>::BYTES, AttendSmem<D, MB>::ROWS, 2};
+}
 template <int DT, int D, int N, bool ALT>
-AttendKernel take() {
-    return {sc_attend_tc_kernel<DT, D, N, ALT>, TC_NT, TcShape<DT, D, N, ALT>::BYTES, N};
+AttendKernel tensor_memory() {
+    return {sc_attend_tc_kernel<DT, D, N, ALT>, TC_NT, TcShape<DT, D, N, ALT>::BYTES, N, 1};
 }
 }  // namespace
 
+#ifndef TC_FROM
+#define TC_FROM 65
+#endif
 template <int DT, int D>
 AttendKernel attend_kernel(int rows) {
-    if (rows <= 16) return take<DT, D, 16, true>();
-    if (rows <= 32) return take<DT, D, 32, true>();
-    if (rows <= 48) return take<DT, D, 48, false>();
-    return take<DT, D, 80, false>();
+    if (rows < TC_FROM) {
+        if (rows <= 16) return warps<DT, D, 1>();
+        if (rows <= 32) return warps<DT, D, 2>();
+        if (rows <= 64) return warps<DT, D, 4>();
+    }
+    if (rows <= 48) return tensor_memory<DT, D, 48, false>();
+    return tensor_memory<DT, D, 80, false>();
 }
 
 template AttendKernel attend_kernel<SC_DT, SC_D>(int rows);

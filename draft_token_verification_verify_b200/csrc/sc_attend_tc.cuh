@@ -59,9 +59,6 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void tc_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 // D (tensor memory, fp32) = A (tensor memory) . B (shared memory) (+ D)
 __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -73,13 +70,14 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 // 16 lanes x 32 columns: a thread writes columns 8 j + 2 (lane % 4) + {0, 1}
 // of the lanes lane / 4 (x[4j], x[4j+1]) and lane / 4 + 8 (x[4j+2], x[4j+3]).
+// (Four narrow stores: one of 16 registers in a row costs the expansion a move
+// for each of them.)
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&x)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(addr),
-        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]),
-        "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
-        : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr + 8 * j),
+                     "r"(x[4 * j]), "r"(x[4 * j + 1]), "r"(x[4 * j + 2]), "r"(x[4 * j + 3])
+                     : "memory");
 }
 // 8 columns of the warp's 32 lanes, one lane a thread.
 __device__ __forceinline__ void tc_ld8(uint32_t addr, float (&x)[8]) {
@@ -112,63 +110,31 @@ __device__ __forceinline__ bool named_or(int id, int threads, bool x) {
         : "=r"(r)
         : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
         : "memory");
-    return r != 0;
+    return __any_sync(0xffffffffu, r);
 }
 __device__ __forceinline__ float warp_max_f32(float x) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
-// Waits for phase `parity` of `bar`; false after about `limit_ns`.  A failed try
-// suspends the thread for a while, so the clock is looked at now and then only.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    uint64_t t0 = 0;
-    for (uint32_t i = 1; i < 0x40000000u; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
-            : "memory");
-        if (ok) return true;
-        if ((i & 15u) == 0u) {
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > limit_ns) return false;
-        }
-    }
-    return false;
+__device__ __forceinline__ bool tc_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
-// fp32 pairs
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t x, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Registers of a group of four warps.  The CTA starts with 640 x 96 = 61,440;
-// 128 x (48 + 80 + 80 + 2 x 136) = 61,440 are given out.
+// 128 x (56 + 72 + 72 + 2 x 136) = 60,416 are given out.
 template <int R>
 __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
@@ -176,12 +142,6 @@ __device__ __forceinline__ void regs_down() {
 template <int R>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // Instruction descriptor: fp32 accumulator, A and B bf16 (1) or fp16 (0), both
@@ -197,11 +157,6 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr) {
            (static_cast<uint64_t>(2) << 61);
 }
 
-// The scalings above as fp32: 2^64, 2^60, 2^69, 2^-69, 2^-64, 2^24.
-constexpr float TC_2P64 = 18446744073709551616.f;
-constexpr float TC_2P60 = 1152921504606846976.f;
-constexpr float TC_2P69 = 590295810358705651712.f;
-
 // N rows a block; ALT: the two softmax groups take turns at the tiles.
 template <int DT, int D, int N_, bool ALT_>
 struct TcShape {
@@ -209,6 +164,7 @@ struct TcShape {
     static constexpr bool ALT = ALT_;
     static constexpr int NC = ALT ? N : N / 2;             // rows of a softmax thread
     static constexpr int ACC = ALT ? 2 : 1;                // output accumulators
+    static constexpr int SR = N <= 48 ? 4 : 2;             // score buffers: tiles the MMAs may run ahead
     static constexpr int GROUP_WARPS = ALT ? 4 : 8;        // softmax warps of a tile
     static constexpr int STAGE = TC_TILE * (D + 8) + 256;  // blocks of 16 or 32 tokens are padded apart
     static constexpr int HALF = N * 128;                   // 64 elements of K for N rows
@@ -222,13 +178,15 @@ struct TcShape {
     static constexpr int OFF_REF = OFF_QS + 2 * N * 4;          // float [2][NC]: minus the reference, 0 when none
     static constexpr int OFF_SET = OFF_REF + 2 * NC * 4;        // float [2][NC]: the reference, -inf when none
     static constexpr int OFF_FAC = OFF_SET + 2 * NC * 4;        // float [2][NC]: a moved reference's factor
-    static constexpr int OFF_DEL = OFF_FAC + 2 * NC * 4;        // float [2][NC]: and its difference
+    static constexpr int OFF_DEL = OFF_FAC + 2 * NC * 4;        // float [2][NC]: sums of p * zero
     static constexpr int OFF_RED = OFF_DEL + 2 * NC * 4;        // float2 [4 warps][2][NC]
-    static constexpr int OFF_MASK = OFF_RED + 4 * 2 * NC * 8;   // uint32 [2][NC][TC_MASK_WORDS]
+    static constexpr int OFF_AT = OFF_RED + 4 * 2 * NC * 8;     // int64 [N]: output rows
+    static constexpr int OFF_MASK = OFF_AT + N * 8;             // uint32 [2][NC][TC_MASK_WORDS]
     static constexpr int OFF_ODD = OFF_MASK + 2 * NC * TC_MASK_WORDS * 4;  // uint32 [2][4 warps][TC_MASK_WORDS]
     static constexpr int OFF_BAD = OFF_ODD + 8 * TC_MASK_WORDS * 4;        // int [TC_STAGES]
-    static constexpr int OFF_BAR = (OFF_BAD + TC_STAGES * 4 + 15) / 16 * 16;
-    static constexpr int BARS = 2 * TC_STAGES + 19;
+    static constexpr int OFF_FLAG = OFF_BAD + TC_STAGES * 4;               // int [2 groups]: a reference has to move
+    static constexpr int OFF_BAR = (OFF_FLAG + 8 + 15) / 16 * 16;
+    static constexpr int BARS = 2 * TC_STAGES + 17 + SR + 2;
     static constexpr int USED = OFF_BAR + BARS * 8 + 16 + 1024;  // + tensor-memory address, error flag; alignment
     // all of tensor memory is allocated, so no second CTA may fit beside this one
     static constexpr int BYTES = USED > 117 * 1024 ? USED : 117 * 1024;
@@ -237,8 +195,8 @@ struct TcShape {
     // tensor memory columns
     static constexpr int T_K = 0;                  // 2 x D / 2
     static constexpr int T_V = T_K + 2 * (D / 2);  // 2 x 64
-    static constexpr int T_S = T_V + 2 * 64;       // 2 x N
-    static constexpr int T_O = T_S + 2 * N;        // ACC x N
+    static constexpr int T_S = T_V + 2 * 64;       // SR x N
+    static constexpr int T_O = T_S + SR * N;       // ACC x N
     static_assert(T_O + ACC * N <= 512, "tensor memory");
 };
 
@@ -262,16 +220,6 @@ __device__ __forceinline__ float tc_sum8(const float* v, int lane) {
     return s + __shfl_xor_sync(0xffffffffu, s, 16);
 }
 
-// Pair j of a word's codes as 16-bit subnormals.  BF16: the odd pairs are 16
-// times their value.
-template <bool BF16>
-__device__ __forceinline__ uint32_t tc_codes(uint32_t w, uint32_t w8, int j) {
-    if constexpr (BF16)
-        return ((j & 2) ? w8 : w) & ((j & 1) ? 0x00F000F0u : 0x000F000Fu);
-    else
-        return (w >> (4 * j)) & 0x000F000Fu;
-}
-
 template <int DT, int D, int N_, bool ALT_>
 __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_constant__ AttendParams P) {
     using Ty = SC<DT>;
@@ -285,13 +233,15 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
     float* qs_s = reinterpret_cast<float*>(base + Sm::OFF_QS);
     volatile int* bad_s = reinterpret_cast<int*>(base + Sm::OFF_BAD);
     uint32_t* odd_s = reinterpret_cast<uint32_t*>(base + Sm::OFF_ODD);
+    volatile int* flag_s = reinterpret_cast<int*>(base + Sm::OFF_FLAG);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(base + Sm::OFF_BAR);
     uint64_t* raw_empty = raw_full + TC_STAGES;
     uint64_t* ak_full = raw_empty + TC_STAGES;  // expanded keys in tensor memory
     uint64_t* ak_empty = ak_full + 2;
     uint64_t* av_full = ak_empty + 2;           // expanded values
     uint64_t* s_full = av_full + 2;             // scores
-    uint64_t* p_full = s_full + 2;              // weights stored, scores read
+    uint64_t* vote = s_full + Sm::SR;           // a softmax group's warps have looked at a tile's scores
+    uint64_t* p_full = vote + 2;              // weights stored, scores read
     uint64_t* pv_done = p_full + 2;             // frees the weights and the expanded values
     uint64_t* q_full = pv_done + 2;             // a segment's queries
     uint64_t* q_empty = q_full + 2;
@@ -300,7 +250,8 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* err_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the broadcast tells the compiler that a role is a whole warp's)
+    const int tid = threadIdx.x, warp = __shfl_sync(ALL, tid >> 5, 0), lane = tid & 31;
     const int r8 = lane >> 2, q4 = lane & 3;
     const CacheView& c = P.c;
 
@@ -309,24 +260,29 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
     if (tid == 0) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (R.g0 >= R.g1) return;
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < TC_STAGES; ++i) {
             mbar_init(&raw_full[i], 1);
             mbar_init(&raw_empty[i], 8 + Sm::GROUP_WARPS);
         }
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ak_full[i], 4);
             mbar_init(&ak_empty[i], 1);
             mbar_init(&av_full[i], 4);
-            mbar_init(&s_full[i], 1);
+            mbar_init(&vote[i], 4);
             mbar_init(&p_full[i], Sm::GROUP_WARPS);
             mbar_init(&pv_done[i], 1);
             mbar_init(&q_full[i], 4);
             mbar_init(&q_empty[i], 8);
             mbar_init(&odd_full[i], 4);
         }
+#pragma unroll 1
+        for (int i = 0; i < Sm::SR; ++i) mbar_init(&s_full[i], 1);
         mbar_init(done, 1);
         fence_mbar_init();
         *err_s = 0;
+        flag_s[0] = flag_s[1] = 0;
     }
     if (warp == 17) {
         tc_alloc(tmem_slot, 512);
@@ -352,7 +308,7 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
     auto cached = [&](int u) { return u * TC_TILE < w.len; };
     auto active = [&]() { return w.len > 0 || P.k_new != nullptr; };
 
-    if (warp >= 16) regs_down<48>();
+    if (warp >= 16) regs_down<56>();
     if (warp == 16) {
         // ---- the copies ----
         unsigned char* raw = base + Sm::OFF_RAW;
@@ -363,13 +319,15 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                        ? __ldg(c.table + static_cast<size_t>(w.b) * c.max_pages + (t >> c.log2_page))
                        : -2;
         };
+#pragma unroll 1
         for (bool go = true; go && !failed; go = w.next(P)) {
             const int head = w.hr / P.row_blocks;
             int sub, id = page(w.u0, &sub);
+#pragma unroll 1
             for (int u = w.u0; u < w.u1 && cached(u); ++u) {
                 const int s = ir % TC_STAGES;
                 if (ir >= TC_STAGES &&
-                    !__all_sync(ALL, tc_wait(&raw_empty[s], ((ir / TC_STAGES) - 1) & 1, P.timeout_ns))) {
+                    !sc_wait(&raw_empty[s], ((ir / TC_STAGES) - 1) & 1, P.timeout_ns)) {
                     failed = true;
                     break;
                 }
@@ -388,76 +346,89 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
             }
         }
         // no copy may land after the CTA is gone
+#pragma unroll 1
         for (int i = ir > TC_STAGES ? ir - TC_STAGES : 0; i < ir; ++i)
-            if (!tc_wait(&raw_full[i % TC_STAGES], (i / TC_STAGES) & 1, P.timeout_ns)) failed = true;
+            if (!sc_wait(&raw_full[i % TC_STAGES], (i / TC_STAGES) & 1, P.timeout_ns)) failed = true;
     } else if (warp == 17) {
-        // ---- the MMAs: S of a tile, then O of the tile before it; the warp stays
+        // ---- the MMAs: whichever product has its operands, O first; the warp stays
         // together and one elected lane issues, so that the operands are uniform ----
         constexpr uint32_t id_qk = tc_idesc(DT == 0, N), id_pv = tc_idesc(1, N);
         const bool leader = elect_one();
         const uint64_t q_desc = tc_desc(smem_u32(base)), p_desc = tc_desc(smem_u32(base + Sm::OFF_P));
-        bool have = false, dense = false, first = false;  // of the tile before
-        auto pv = [&](int i) {                            // the PV product of tile i
-            const int b = i & 1;
-            if (!__all_sync(ALL, tc_wait(&av_full[b], (i >> 1) & 1, P.timeout_ns) &&
-                                     tc_wait(&p_full[b], (i >> 1) & 1, P.timeout_ns))) {
-                failed = true;
-                return;
-            }
-            tc_after();
-            if (leader) {
-                const uint32_t a = tmem + Sm::T_V + b * 64, o = tmem + Sm::T_O + (ALT ? b * N : 0);
-                const uint64_t pd = p_desc + static_cast<uint64_t>(b * (Sm::PB >> 4));
-                if constexpr (DT == 0) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc_mma(o, a + 8 * k, pd + ((k >> 2) * Sm::HALF + (k & 3) * 32) / 16, id_pv,
-                               (first && k == 0) ? 0u : 1u);
-                } else {
-                    // scored positions keep the activations' type; the codes are bf16, and their
-                    // weights come in two parts
-                    const uint32_t idesc = dense ? id_qk : id_pv;
-                    for (int part = 0; part < (dense ? 1 : Sm::PSPLIT); ++part)
+        int qi = 0, pi = 0;              // the next tile's S, and O
+        uint32_t firsts = 0, denses = 0;  // bit i & 31: of tile i
+        bool more = true;                // tiles left to score
+        while (more && !active()) more = w.next(P);
+        int u = w.u0;
+        uint64_t t0 = 0;
+        uint32_t idle = 0;
+#pragma unroll 1
+        while ((more || pi < qi) && !failed) {
+            bool did = false;
+            if (pi < qi && tc_test(&p_full[pi & 1], (pi >> 1) & 1) && tc_test(&av_full[pi & 1], (pi >> 1) & 1)) {
+                const int b = pi & 1;
+                const bool dense = (denses >> (pi & 31)) & 1u, first = (firsts >> (pi & 31)) & 1u;
+                tc_after();
+                if (leader) {
+                    const uint32_t a = tmem + Sm::T_V + b * 64, o = tmem + Sm::T_O + (ALT ? b * N : 0);
+                    const uint64_t pd = p_desc + static_cast<uint64_t>(b * (Sm::PB >> 4));
+                    // with fp16 activations the scored positions keep their type; the codes are
+                    // bf16, and their weights come in two parts
+                    const uint32_t idesc = DT == 1 && dense ? id_qk : id_pv;
+                    const int parts = DT == 1 && dense ? 1 : Sm::PSPLIT;
+#pragma unroll 1
+                    for (int part = 0; part < parts; ++part)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             tc_mma(o, a + 8 * k, pd + (part * 2 * Sm::HALF + (k >> 2) * Sm::HALF + (k & 3) * 32) / 16, idesc,
                                    (first && part == 0 && k == 0) ? 0u : 1u);
-                }
-                tc_commit(&pv_done[b]);
-            }
-            __syncwarp();
-        };
-        for (bool go = true; go && !failed; go = w.next(P)) {
-            if (!active()) continue;
-            const uint64_t qd = q_desc + static_cast<uint64_t>((seg & 1) * (Sm::Q >> 4));
-            for (int u = w.u0; u < w.u1 && !failed; ++u, ++it) {
-                const int b = it & 1;
-                if (!__all_sync(ALL, tc_wait(&ak_full[b], (it >> 1) & 1, P.timeout_ns))) {
-                    failed = true;
-                    break;
-                }
-                // (S of tile it - 2 has been read: its weights were waited for in pv(it - 2))
-                tc_after();
-                if (leader) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma(tmem + Sm::T_S + b * N, tmem + Sm::T_K + b * (D / 2) + 8 * k,
-                               qd + ((k >> 2) * Sm::HALF + (k & 3) * 32) / 16, id_qk, k != 0);
-                    tc_commit(&ak_empty[b]);
-                    tc_commit(&s_full[b]);
+                    tc_commit(&pv_done[b]);
                 }
                 __syncwarp();
-                if (have) pv(it - 1);
-                have = true;
-                dense = !cached(u);
-                first = u - w.u0 < Sm::ACC;
+                ++pi;
+                did = true;
             }
-            ++seg;
+            // (the scores of tile qi - SR have been read once its weights are there)
+            if (more && qi - pi < Sm::SR && tc_test(&ak_full[qi & 1], (qi >> 1) & 1)) {
+                const int b = qi & 1;
+                tc_after();
+                if (leader) {
+                    const uint64_t qd = q_desc + static_cast<uint64_t>((seg & 1) * (Sm::Q >> 4));
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma(tmem + Sm::T_S + (qi % Sm::SR) * N, tmem + Sm::T_K + b * (D / 2) + 8 * k,
+                               qd + ((k >> 2) * Sm::HALF + (k & 3) * 32) / 16, id_qk, k != 0);
+                    tc_commit(&ak_empty[b]);
+                    tc_commit(&s_full[qi % Sm::SR]);
+                }
+                __syncwarp();
+                const uint32_t bit = 1u << (qi & 31);
+                firsts = u - w.u0 < Sm::ACC ? firsts | bit : firsts & ~bit;
+                denses = cached(u) ? denses & ~bit : denses | bit;
+                ++qi;
+                if (++u == w.u1) {
+                    ++seg;
+                    do more = w.next(P);
+                    while (more && !active());
+                    u = w.u0;
+                }
+                did = true;
+            }
+            if (did) {
+                idle = 0;
+            } else {
+                __nanosleep(64);
+                if ((++idle & 63u) == 0u) {  // nothing for a while: mind the clock
+                    const uint64_t now = globaltimer_ns();
+                    if (idle == 64u) t0 = now;
+                    if (now - t0 > P.timeout_ns) failed = true;
+                }
+                failed = __any_sync(ALL, failed);
+            }
         }
-        if (have && !failed) pv(it - 1);
         if (leader) tc_commit(done);
     } else if (warp < 4) {
-        regs_down<80>();
+        regs_down<72>();
         // ---- keys: queries of a segment, then codes to tensor memory ----
         // a lane's tokens are 32 warp + 8 i + r8; its bytes of tokens i = 0 and 2 (1 and 3 lie 8 rows on)
         uint32_t off[2];
@@ -466,15 +437,17 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
             const int t = 32 * warp + 16 * i + r8;
             off[i] = (t >> c.log2_block) * bstride + (t & (c.block - 1)) * (D / 2) + q4 * (D / 8);
         }
+#pragma unroll 1
         for (bool go = true; go && !failed; go = w.next(P)) {
             if (!active()) continue;
             const int head = w.hr / P.row_blocks, row0 = (w.hr % P.row_blocks) * N, qb = seg & 1;
-            if (seg >= 2 && !__all_sync(ALL, tc_wait(&q_empty[qb], ((seg >> 1) - 1) & 1, P.timeout_ns))) {
+            if (seg >= 2 && !sc_wait(&q_empty[qb], ((seg >> 1) - 1) & 1, P.timeout_ns)) {
                 failed = true;
                 break;
             }
             // column 8 j + 2 q + e of the key operand holds the dims (D / 4) q + 4 j + 2 e, + 1:
             // the queries take the same order
+#pragma unroll 1
             for (int i = tid; i < N * (D / 8); i += 128) {
                 const int r = i / (D / 8), ch = i % (D / 8), row = row0 + r;
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -485,10 +458,10 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                     const uint2 lo = *reinterpret_cast<const uint2*>(src), hi = *reinterpret_cast<const uint2*>(src + D / 4);
                     x = make_uint4(lo.x, lo.y, hi.x, hi.y);
                     if constexpr (DT == 0) {  // 2^64, and 2^60 where the code is 16-fold (exact)
-                        x.x = Ty::pack(Ty::lo(x.x) * TC_2P64, Ty::hi(x.x) * TC_2P64);
-                        x.y = Ty::pack(Ty::lo(x.y) * TC_2P60, Ty::hi(x.y) * TC_2P60);
-                        x.z = Ty::pack(Ty::lo(x.z) * TC_2P64, Ty::hi(x.z) * TC_2P64);
-                        x.w = Ty::pack(Ty::lo(x.w) * TC_2P60, Ty::hi(x.w) * TC_2P60);
+                        x.x = Ty::pack(Ty::lo(x.x) * SC_2P64, Ty::hi(x.x) * SC_2P64);
+                        x.y = Ty::pack(Ty::lo(x.y) * SC_2P60, Ty::hi(x.y) * SC_2P60);
+                        x.z = Ty::pack(Ty::lo(x.z) * SC_2P64, Ty::hi(x.z) * SC_2P64);
+                        x.w = Ty::pack(Ty::lo(x.w) * SC_2P60, Ty::hi(x.w) * SC_2P60);
                     }
                 }
                 *reinterpret_cast<uint4*>(base + qb * Sm::Q + (ch >> 3) * Sm::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
@@ -511,86 +484,98 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
             }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) tc_arrive(&q_full[qb]);
-            for (int u = w.u0; u < w.u1; ++u, ++it) {
+            if (lane == 0) sc_arrive(&q_full[qb]);
+            int u = w.u0;
+            const int uc = min(w.u1, (w.len + TC_TILE - 1) / TC_TILE);  // behind the cache tiles
+#pragma unroll 1
+            for (; u < uc; ++u, ++it, ++ir) {
                 const int b = it & 1;
-                const bool code = cached(u);
-                bool got = it < 2 || tc_wait(&ak_empty[b], ((it >> 1) - 1) & 1, P.timeout_ns);
-                if (code) got = got && tc_wait(&raw_full[ir % TC_STAGES], (ir / TC_STAGES) & 1, P.timeout_ns);
-                if (!__all_sync(ALL, got)) {
+                if (!(it < 2 || sc_wait(&ak_empty[b], ((it >> 1) - 1) & 1, P.timeout_ns)) ||
+                    !sc_wait(&raw_full[ir % TC_STAGES], (ir / TC_STAGES) & 1, P.timeout_ns)) {
                     failed = true;
                     break;
                 }
                 tc_after();
                 const uint32_t dst = tmem + Sm::T_K + b * (D / 2) + (static_cast<uint32_t>(32 * warp) << 16);
-                if (code) {
-                    const unsigned char* tile = base + Sm::OFF_RAW + (ir % TC_STAGES) * Sm::STAGE;
-                    uint32_t kw[4][D / 32];
+                const unsigned char* tile = base + Sm::OFF_RAW + (ir % TC_STAGES) * Sm::STAGE;
+                uint32_t kw[4][D / 32];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const unsigned char* a = tile + off[i >> 1] + (i & 1) * 8 * (D / 2);
-                        if constexpr (D == 128) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(a);
-                            kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
-                        } else {
-                            const uint2 v = *reinterpret_cast<const uint2*>(a);
-                            kw[i][0] = v.x, kw[i][1] = v.y;
-                        }
+                for (int i = 0; i < 4; ++i) {
+                    const unsigned char* a = tile + off[i >> 1] + (i & 1) * 8 * (D / 2);
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(a);
+                        kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(a);
+                        kw[i][0] = v.x, kw[i][1] = v.y;
                     }
+                }
 #pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2)
+                for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
-                        for (int s = 0; s < D / 64; ++s) {
-                            uint32_t x[16];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    const uint32_t wd = kw[2 * h2 + y][2 * s + k], w8 = wd >> 8;
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        x[8 * k + 4 * (j >> 1) + 2 * y + (j & 1)] = tc_codes<DT == 0>(wd, w8, j);
-                                }
-                            tc_st16(dst + (static_cast<uint32_t>(16 * h2) << 16) + 32 * s, x);
-                        }
-                    __syncwarp();
-                    if (lane == 0) tc_arrive(&raw_empty[ir % TC_STAGES]);
-                    ++ir;
-                } else {
-                    const int j0 = (u - (w.len + TC_TILE - 1) / TC_TILE) * TC_TILE;
-#pragma unroll 1
-                    for (int hs = 0; hs < 2 * (D / 64); ++hs) {
-                        const int h2 = hs / (D / 64), s = hs % (D / 64);
+                    for (int s = 0; s < D / 64; ++s) {
                         uint32_t x[16];
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int j = j0 + 32 * warp + 16 * h2 + 8 * y + r8;
-                            const T* src = static_cast<const T*>(P.k_new) + (static_cast<long long>(w.b) * P.n + j) * P.kv_stride +
-                                           static_cast<long long>(head) * D + q4 * (D / 4) + 16 * s;
+                        for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                uint4 v = j < P.n ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-                                if constexpr (DT == 0) {  // against the queries' 2^60
-                                    v.y = Ty::pack(Ty::lo(v.y) * 16.f, Ty::hi(v.y) * 16.f);
-                                    v.w = Ty::pack(Ty::lo(v.w) * 16.f, Ty::hi(v.w) * 16.f);
-                                }
-                                x[8 * i + 2 * y] = v.x, x[8 * i + 2 * y + 1] = v.y;
-                                x[8 * i + 4 + 2 * y] = v.z, x[8 * i + 4 + 2 * y + 1] = v.w;
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t wd = kw[2 * h2 + y][2 * s + k], w8 = wd >> 8;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    x[8 * k + 4 * (j >> 1) + 2 * y + (j & 1)] = sc_codes<DT == 0>(wd, w8, j);
                             }
-                        }
-                        __syncwarp();
                         tc_st16(dst + (static_cast<uint32_t>(16 * h2) << 16) + 32 * s, x);
                     }
+                tc_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) {
+                    sc_arrive(&raw_empty[ir % TC_STAGES]);
+                    sc_arrive(&ak_full[b]);
+                }
+            }
+#pragma unroll 1
+            for (; u < w.u1 && !failed; ++u, ++it) {
+                const int b = it & 1;
+                if (it >= 2 && !sc_wait(&ak_empty[b], ((it >> 1) - 1) & 1, P.timeout_ns)) {
+                    failed = true;
+                    break;
+                }
+                tc_after();
+                const uint32_t dst = tmem + Sm::T_K + b * (D / 2) + (static_cast<uint32_t>(32 * warp) << 16);
+                const int j0 = (u - (w.len + TC_TILE - 1) / TC_TILE) * TC_TILE;
+#pragma unroll 1
+                for (int hs = 0; hs < 2 * (D / 64); ++hs) {
+                    const int h2 = hs / (D / 64), s = hs % (D / 64);
+                    uint32_t x[16];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int j = j0 + 32 * warp + 16 * h2 + 8 * y + r8;
+                        const T* src = static_cast<const T*>(P.k_new) + (static_cast<long long>(w.b) * P.n + j) * P.kv_stride +
+                                       static_cast<long long>(head) * D + q4 * (D / 4) + 16 * s;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint4 v = j < P.n ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                            if constexpr (DT == 0) {  // against the queries' 2^60
+                                v.y = Ty::pack(Ty::lo(v.y) * 16.f, Ty::hi(v.y) * 16.f);
+                                v.w = Ty::pack(Ty::lo(v.w) * 16.f, Ty::hi(v.w) * 16.f);
+                            }
+                            x[8 * i + 2 * y] = v.x, x[8 * i + 2 * y + 1] = v.y;
+                            x[8 * i + 4 + 2 * y] = v.z, x[8 * i + 4 + 2 * y + 1] = v.w;
+                        }
+                    }
+                    __syncwarp();
+                    tc_st16(dst + (static_cast<uint32_t>(16 * h2) << 16) + 32 * s, x);
                 }
                 tc_wait_st();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) tc_arrive(&ak_full[b]);
+                if (lane == 0) sc_arrive(&ak_full[b]);
             }
             ++seg;
         }
     } else if (warp < 8) {
-        regs_down<80>();
+        regs_down<72>();
         // ---- values: codes to tensor memory, a lane of it a dim ----
         const int wq = warp & 3;
         uint32_t off[2];  // this lane's 16 tokens of each 64, in the rows of dim 32 wq + r8
@@ -601,99 +586,110 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                       (32 * wq + r8) * (c.block / 2);
         }
         const uint32_t rows8 = 8 * (c.block / 2);
+#pragma unroll 1
         for (bool go = true; go && !failed; go = w.next(P)) {
             if (!active()) continue;
             const int head = w.hr / P.row_blocks;
-            if (seg >= 2 && !__all_sync(ALL, tc_wait(&q_empty[seg & 1], ((seg >> 1) - 1) & 1, P.timeout_ns))) {
+            if (seg >= 2 && !sc_wait(&q_empty[seg & 1], ((seg >> 1) - 1) & 1, P.timeout_ns)) {
                 failed = true;
                 break;
             }
-            bool dense = false;
-            for (int u = w.u0; u < w.u1; ++u, ++it) {
+            int u = w.u0;
+            const int uc = min(w.u1, (w.len + TC_TILE - 1) / TC_TILE);
+#pragma unroll 1
+            for (; u < uc; ++u, ++it, ++ir) {
                 const int b = it & 1;
-                const bool code = cached(u);
-                bool got = it < 2 || tc_wait(&pv_done[b], ((it >> 1) - 1) & 1, P.timeout_ns);
-                if (code) got = got && tc_wait(&raw_full[ir % TC_STAGES], (ir / TC_STAGES) & 1, P.timeout_ns);
-                if (!__all_sync(ALL, got)) {
+                if (!(it < 2 || sc_wait(&pv_done[b], ((it >> 1) - 1) & 1, P.timeout_ns)) ||
+                    !sc_wait(&raw_full[ir % TC_STAGES], (ir / TC_STAGES) & 1, P.timeout_ns)) {
                     failed = true;
                     break;
                 }
                 tc_after();
-                const uint32_t dst = tmem + Sm::T_V + b * 64 + (static_cast<uint32_t>(32 * wq) << 16);
-                if (code) {
-                    if (32 * wq < D) {
-                        const unsigned char* tile = base + Sm::OFF_RAW + (ir % TC_STAGES) * Sm::STAGE;
+                if (32 * wq < D) {
+                    const uint32_t dst = tmem + Sm::T_V + b * 64 + (static_cast<uint32_t>(32 * wq) << 16);
+                    const unsigned char* tile = base + Sm::OFF_RAW + (ir % TC_STAGES) * Sm::STAGE;
+                    uint2 v[2][4];
 #pragma unroll
-                        for (int hb = 0; hb < 2; ++hb) {
-                            uint2 v[4];
+                    for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint2*>(tile + off[hb] + i * rows8);
+                        for (int i = 0; i < 4; ++i) v[hb][i] = *reinterpret_cast<const uint2*>(tile + off[hb] + i * rows8);
 #pragma unroll
-                            for (int h2 = 0; h2 < 2; ++h2) {
-                                uint32_t x[16];
+                    for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                    for (int y = 0; y < 2; ++y) {
-                                        const uint32_t wd = k ? v[2 * h2 + y].y : v[2 * h2 + y].x, w8 = wd >> 8;
-#pragma unroll
-                                        for (int j = 0; j < 4; ++j)
-                                            x[8 * k + 4 * (j >> 1) + 2 * y + (j & 1)] =
-                                                DT == 0 ? tc_codes<true>(wd, w8, j) : sc_center_bf16(sc_codes_bf16(wd, j));
-                                    }
-                                tc_st16(dst + (static_cast<uint32_t>(16 * h2) << 16) + 32 * hb, x);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                    if (lane == 0) tc_arrive(&raw_empty[ir % TC_STAGES]);
-                    ++ir;
-                } else {
-                    // the scored positions' own values; an element that is not finite is left out of
-                    // the product, where it would reach the rows that do not see it, and noted
-                    uint32_t* odd = odd_s + ((dseg & 1) * 4 + wq) * TC_MASK_WORDS;
-                    if (!dense && lane < TC_MASK_WORDS) odd[lane] = 0u;
-                    dense = true;
-                    __syncwarp();
-                    const int j0 = (u - (w.len + TC_TILE - 1) / TC_TILE) * TC_TILE;
-                    if (32 * wq < D) {
-#pragma unroll 1
-                        for (int hh = 0; hh < 4; ++hh) {
-                            const int hb = hh >> 1, h2 = hh & 1;
+                        for (int h2 = 0; h2 < 2; ++h2) {
                             uint32_t x[16];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
+                            for (int k = 0; k < 2; ++k)
 #pragma unroll
                                 for (int y = 0; y < 2; ++y) {
-                                    uint32_t pair = 0u;
+                                    const uint32_t wd = k ? v[hb][2 * h2 + y].y : v[hb][2 * h2 + y].x, w8 = wd >> 8;
 #pragma unroll
-                                    for (int f = 0; f < 2; ++f) {
-                                        const int j = j0 + 64 * hb + 16 * q4 + 2 * i + f;
-                                        if (j < P.n) {
-                                            const uint16_t e = reinterpret_cast<const uint16_t*>(P.v_new)
-                                                [(static_cast<long long>(w.b) * P.n + j) * P.kv_stride +
-                                                 static_cast<long long>(head) * D + 32 * wq + 16 * h2 + 8 * y + r8];
-                                            if (fabsf(Ty::lo(e)) < __builtin_huge_valf())
-                                                pair |= static_cast<uint32_t>(e) << (16 * f);
-                                            else
-                                                atomicOr(&odd[j >> 5], 1u << (j & 31));
-                                        }
-                                    }
-                                    x[4 * (i >> 1) + 2 * y + (i & 1)] = pair;
+                                    for (int j = 0; j < 4; ++j)
+                                        x[8 * k + 4 * (j >> 1) + 2 * y + (j & 1)] =
+                                            DT == 0 ? sc_codes<true>(wd, w8, j) : sc_center_bf16(sc_codes_bf16(wd, j));
                                 }
-                            __syncwarp();
                             tc_st16(dst + (static_cast<uint32_t>(16 * h2) << 16) + 32 * hb, x);
                         }
+                    tc_wait_st();
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) {
+                    sc_arrive(&raw_empty[ir % TC_STAGES]);
+                    sc_arrive(&av_full[b]);
+                }
+            }
+            const bool dense = u < w.u1;
+            // the scored positions' own values; an element that is not finite is left out of
+            // the product, where it would reach the rows that do not see it, and noted
+            uint32_t* odd = odd_s + ((dseg & 1) * 4 + wq) * TC_MASK_WORDS;
+            if (dense && lane < TC_MASK_WORDS) odd[lane] = 0u;
+#pragma unroll 1
+            for (; u < w.u1 && !failed; ++u, ++it) {
+                const int b = it & 1;
+                if (it >= 2 && !sc_wait(&pv_done[b], ((it >> 1) - 1) & 1, P.timeout_ns)) {
+                    failed = true;
+                    break;
+                }
+                tc_after();
+                __syncwarp();
+                const uint32_t dst = tmem + Sm::T_V + b * 64 + (static_cast<uint32_t>(32 * wq) << 16);
+                const int j0 = (u - (w.len + TC_TILE - 1) / TC_TILE) * TC_TILE;
+                if (32 * wq < D) {
+#pragma unroll 1
+                    for (int hh = 0; hh < 4; ++hh) {
+                        const int hb = hh >> 1, h2 = hh & 1;
+                        uint32_t x[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = 0u;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int j1 = j0 + 64 * hb + 16 * q4;  // this lane's 16 positions
+                            const uint16_t* src = static_cast<const uint16_t*>(P.v_new) +
+                                                  (static_cast<long long>(w.b) * P.n + j1) * P.kv_stride +
+                                                  static_cast<long long>(head) * D + 32 * wq + 16 * h2 + 8 * y + r8;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                uint32_t e = j1 + i < P.n ? src[i * P.kv_stride] : 0u;
+                                if (!(fabsf(Ty::lo(e)) < __builtin_huge_valf())) {
+                                    atomicOr(&odd[(j1 + i) >> 5], 1u << ((j1 + i) & 31));
+                                    e = 0u;
+                                }
+                                x[4 * (i >> 2) + 2 * y + ((i >> 1) & 1)] |= e << (16 * (i & 1));
+                            }
+                        }
+                        __syncwarp();
+                        tc_st16(dst + (static_cast<uint32_t>(16 * h2) << 16) + 32 * hb, x);
                     }
                 }
                 tc_wait_st();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) tc_arrive(&av_full[b]);
+                if (lane == 0) sc_arrive(&av_full[b]);
             }
             if (dense) {
                 __syncwarp();
-                if (lane == 0 && !failed) tc_arrive(&odd_full[dseg & 1]);
+                if (lane == 0 && !failed) sc_arrive(&odd_full[dseg & 1]);
                 ++dseg;
             }
             ++seg;
@@ -706,7 +702,6 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
         float* ref_s = reinterpret_cast<float*>(base + Sm::OFF_REF) + half * NC;
         float* set_s = reinterpret_cast<float*>(base + Sm::OFF_SET) + half * NC;
         float* fac_s = reinterpret_cast<float*>(base + Sm::OFF_FAC) + half * NC;
-        float* del_s = reinterpret_cast<float*>(base + Sm::OFF_DEL) + half * NC;
         float2* red_s = reinterpret_cast<float2*>(base + Sm::OFF_RED) + half * NC;
         constexpr int RS = 2 * NC;  // of red_s, from warp to warp
         uint32_t* mask_s = reinterpret_cast<uint32_t*>(base + Sm::OFF_MASK) + half * NC * TC_MASK_WORDS;
@@ -721,13 +716,15 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
         const float sl = P.scale * SC_LOG2E;
         const float nan = __int_as_float(0x7fffffff);
         // what a code's product, a scored position's product and a weight are multiplied by
-        const float k_code = DT == 0 ? TC_2P69 : 16777216.f;
-        const float k_new = DT == 0 ? 1.f / TC_2P64 : 1.f;
-        const float v_code = DT == 0 ? ((t & 2) ? TC_2P60 : TC_2P64) : 1.f;
+        const float k_code = DT == 0 ? SC_2P69 : 16777216.f;
+        const float k_new = DT == 0 ? 1.f / SC_2P64 : 1.f;
+        const float v_code = DT == 0 ? ((t & 2) ? SC_2P60 : SC_2P64) : 1.f;
         const float v_off = -8.f / v_code;
-        const float v_new = DT == 0 ? 1.f / TC_2P69 : 1.f;
-        const float o_scale = DT == 0 ? TC_2P69 : 1.f;
+        const float v_new = DT == 0 ? 1.f / SC_2P69 : 1.f;
+        const float o_scale = DT == 0 ? SC_2P69 : 1.f;
+        uint32_t votes = 0;
 
+#pragma unroll 1
         for (bool go = true; go; go = w.next(P)) {
             const int head = w.hr / P.row_blocks, row0 = (w.hr % P.row_blocks) * N + col0;  // this thread's first row
             uint64_t l[NC / 2], z[NC / 2];
@@ -744,20 +741,24 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
             }
             named_sync(bar, 128);
             const bool act = active();
-            bool unset = true, fresh = true, dense = false;
-            if (act && !failed && !tc_wait(&q_full[seg & 1], (seg >> 1) & 1, P.timeout_ns)) failed = true;
+            bool unset = true, fresh = true, dense = false;  // a row without reference; no weights yet; scored positions
+            if (act && !failed && !sc_wait(&q_full[seg & 1], (seg >> 1) & 1, P.timeout_ns)) failed = true;
             const int it0 = it;
-            for (int u = w.u0; act && u < w.u1; ++u, ++it) {
-                const int b = it & 1;
+            const int tiles = act ? w.u1 - w.u0 : 0;
+            const float* qs = qs_s + (seg & 1) * N + col0;
+#pragma unroll 1
+            for (int u = w.u0; u < w.u0 + tiles; ++u, ++it) {
                 const bool code = cached(u);
-                const int s = ir % TC_STAGES;
+                const int stage = ir % TC_STAGES;
                 const uint32_t raw_phase = (ir / TC_STAGES) & 1;
-                if (code) ++ir;
-                if (!code && !dense) {  // who sees whom, for these rows
+                if (code) {
+                    ++ir;
+                } else if (!dense) {  // scored positions: who sees whom, for these rows
                     dense = true;
                     const int32_t* par = P.parents ? P.parents + static_cast<size_t>(w.b) * (P.n - 1) : nullptr;
                     int wrong = 0;
                     if (par)
+#pragma unroll 1
                         for (int i = 1 + tt; i < P.n; i += 128) wrong |= par[i - 1] < 0 || par[i - 1] >= i;
                     const bool no_tree = named_or(bar, 128, wrong != 0);
                     if (no_tree) poison();
@@ -765,12 +766,13 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                         uint32_t* m = mask_s + tt * TC_MASK_WORDS;
                         const int row = row0 + tt, node = row / P.group;
                         const bool all = !par || no_tree || row >= P.rows;
-                        for (int i = 0; i < TC_MASK_WORDS; ++i) {
-                            // rows behind the last see everything; without parents node i sees 0 .. i
-                            const int hi = row < P.rows ? node : P.n;
+                        // rows behind the last see everything; without parents node i sees 0 .. i
+                        const int hi = row < P.rows ? node : P.n;
+#pragma unroll 1
+                        for (int i = 0; i < TC_MASK_WORDS; ++i)
                             m[i] = !all || i * 32 > hi ? 0u : hi - i * 32 >= 31 ? ALL : (2u << (hi - i * 32)) - 1u;
-                        }
                         if (!all)
+#pragma unroll 1
                             for (int a = node;; a = par[a - 1]) {
                                 m[a >> 5] |= 1u << (a & 31);
                                 if (a == 0) break;
@@ -778,121 +780,132 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                     }
                     named_sync(bar, 128);
                 }
+                const int b = it & 1, sb = it % Sm::SR;
                 if (ALT && b != half) continue;
-                if (!failed && !tc_wait(&s_full[b], (it >> 1) & 1, P.timeout_ns)) failed = true;
-                float ka = sl * k_new, kb = 0.f, vs = v_new, vz = 0.f;
-                int valid;  // tokens of the tile
-                int j0 = 0;
+                float ka = sl * k_new, kb = 0.f, vs = v_new, vz = 0.f, off = 0.f;
+                int valid, j0 = 0;  // tokens of the tile; its first scored position
                 if (code) {
-                    if (!failed && !tc_wait(&raw_full[s], raw_phase, P.timeout_ns)) failed = true;
-                    valid = w.len - u * TC_TILE < TC_TILE ? w.len - u * TC_TILE : TC_TILE;
-                    const unsigned char* par = base + Sm::OFF_RAW + s * Sm::STAGE + poff;
+                    valid = w.len - u * TC_TILE;
+                    if (!failed && !sc_wait(&raw_full[stage], raw_phase, P.timeout_ns)) failed = true;
+                    const unsigned char* par = base + Sm::OFF_RAW + stage * Sm::STAGE + poff;
                     const uint32_t kp = *reinterpret_cast<const uint32_t*>(par);
                     const uint32_t vp = *reinterpret_cast<const uint32_t*>(par + sc_half_bytes<D>(c.block));
-                    const bool bad = bad_s[s] != 0;
+                    const bool bad = __any_sync(ALL, bad_s[stage]);
                     __syncwarp();
-                    if (lane == 0) tc_arrive(&raw_empty[s]);
+                    if (lane == 0) sc_arrive(&raw_empty[stage]);
                     if (bad) poison();
-                    const float k1 = Ty::lo(kp) * sl;
-                    ka = k1 * k_code;
+                    ka = Ty::lo(kp) * sl * k_code;
                     kb = Ty::hi(kp) * sl;
                     vs = Ty::lo(vp);
-                    vz = Ty::hi(vp);
-                    vz = fmaf(8.f, vs, vz);  // the values' middle: codes count from 8
+                    vz = fmaf(8.f, vs, Ty::hi(vp));  // the values' middle: codes count from 8
                     vs *= v_code;
+                    off = v_off;
                     if (t >= valid) ka = kb = vs = vz = 0.f;
                 } else {
                     j0 = (u - (w.len + TC_TILE - 1) / TC_TILE) * TC_TILE;
-                    valid = P.n - j0 < TC_TILE ? P.n - j0 : TC_TILE;
+                    valid = P.n - j0;
                 }
+                if (!failed && !sc_wait(&s_full[sb], (it / Sm::SR) & 1, P.timeout_ns)) failed = true;
+                __syncwarp();
                 tc_after();
-                // scores relative to the reference: scale (q . code) + zero sum(q) - reference
-                float d[NC];
+                const uint32_t s_addr = tmem + Sm::T_S + sb * N + col0 + lane_base;
+                const uint64_t a2 = f2_pack(ka, ka), b2 = f2_pack(kb, kb);
+                const bool special = !code || valid < TC_TILE;
+                // scores of 8 rows relative to the reference: scale (q . code) + zero sum(q) - reference
+                auto relative = [&](float* d, int i0) {
 #pragma unroll
-                for (int g = 0; g < NC / 8; ++g) {
-                    float x[8];
-                    tc_ld8(tmem + Sm::T_S + b * N + col0 + 8 * g + lane_base, x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) d[8 * g + i] = x[i];
-                }
-                tc_wait_ld();
-                float top = SC_NEG_INF;
-                {
-                    const uint64_t a2 = f2_pack(ka, ka), b2 = f2_pack(kb, kb);
-                    const float* qs = qs_s + (seg & 1) * N + col0;
-#pragma unroll
-                    for (int i = 0; i < NC; i += 4) {
-                        const ulonglong2 q2 = *reinterpret_cast<const ulonglong2*>(qs + i);
-                        const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(ref_s + i);
+                    for (int i = 0; i < 8; i += 4) {
+                        const ulonglong2 q2 = *reinterpret_cast<const ulonglong2*>(qs + i0 + i);
+                        const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(ref_s + i0 + i);
                         const uint64_t x = f2_fma(a2, f2_pack(d[i], d[i + 1]), f2_fma(b2, q2.x, n2.x));
                         const uint64_t y = f2_fma(a2, f2_pack(d[i + 2], d[i + 3]), f2_fma(b2, q2.y, n2.y));
                         f2_unpack(x, d[i], d[i + 1]);
                         f2_unpack(y, d[i + 2], d[i + 3]);
                     }
-                }
-                if (!code) {
-                    const int word = (j0 >> 5) + wq;  // of the masks: this warp's 32 positions
+                    if (special) {  // the last cache tile, and scored positions
+                        const uint32_t* m = mask_s + i0 * TC_MASK_WORDS + (j0 >> 5) + wq;
 #pragma unroll
-                    for (int i = 0; i < NC; ++i)
-                        if (!((mask_s[i * TC_MASK_WORDS + word] >> lane) & 1u) || t >= valid) d[i] = SC_NEG_INF;
-                } else if (valid < TC_TILE) {
+                        for (int i = 0; i < 8; ++i)
+                            if (t >= valid || (!code && !((m[i * TC_MASK_WORDS] >> lane) & 1u))) d[i] = SC_NEG_INF;
+                    }
+                };
+                float p[NC];
+#pragma unroll 1
+                for (bool moved = false;; moved = true) {
 #pragma unroll
-                    for (int i = 0; i < NC; ++i)
-                        if (t >= valid) d[i] = SC_NEG_INF;
-                }
+                    for (int g = 0; g < NC; g += 8) tc_ld8(s_addr + g, *reinterpret_cast<float(*)[8]>(p + g));
+                    tc_wait_ld();
+                    float top = SC_NEG_INF;
 #pragma unroll
-                for (int i = 0; i < NC; ++i) top = fmaxf(top, d[i]);
-                // the weights' buffer, and the accumulator a moved reference rescales, are free
-                // when this group's (the tile before last's) product is done
-                if (it >= 2 && !failed && !tc_wait(&pv_done[b], ((it >> 1) - 1) & 1, P.timeout_ns)) failed = true;
-                if (named_or(bar, 128, top > 8.f || failed) || unset) {
+                    for (int g = 0; g < NC; g += 8) {
+                        relative(p + g, g);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) top = fmaxf(top, p[g + i]);
+                    }
+                    // the group's warps vote whether a reference has to move, and go on meanwhile
+                    if (__any_sync(ALL, top > 8.f || failed) && lane == 0) flag_s[half] = 1;
+                    __syncwarp();
+                    if (lane == 0) sc_arrive(&vote[half]);
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) p[i] = ex2(p[i]);
+                    // the weights' buffer, and the accumulator a moved reference rescales, are free
+                    // when this group's (the tile before last's) product is done
+                    if (it >= 2 && !failed && !sc_wait(&pv_done[b], ((it >> 1) - 1) & 1, P.timeout_ns)) failed = true;
+                    // the slowest of the four warps may first have waited for its scores in vain
+                    if (!sc_wait(&vote[half], votes & 1, 4 * P.timeout_ns)) failed = true;
+                    ++votes;
+                    if (moved || !(__any_sync(ALL, flag_s[half]) || unset)) break;
+                    // ---- move the references that have none, or that a score passed by 2^8, and
+                    // look at the tile again (its scores are still in tensor memory) ----
                     if (named_or(bar, 128, failed)) failed = true;
-                    // ---- move the references that have none, or that a score passed by 2^8 ----
+#pragma unroll 1
+                    for (int g = 0; g < NC; g += 8) {
+                        float x[8];
+                        tc_ld8(s_addr + g, x);
+                        tc_wait_ld();
+                        relative(x, g);
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) {
-                        const float mx = warp_max_f32(d[i]);
-                        if (lane == 0) red_s[wq * RS + i].x = mx;
+                        for (int i = 0; i < 8; ++i) {
+                            x[i] = warp_max_f32(x[i]);
+                            if (lane == 0) red_s[wq * RS + g + i].x = x[i];
+                        }
                     }
                     named_sync(bar, 128);
+                    if (tt == 0) flag_s[half] = 0;
                     if (tt < NC) {
                         const float md = fmaxf(fmaxf(red_s[tt].x, red_s[RS + tt].x),
                                                fmaxf(red_s[2 * RS + tt].x, red_s[3 * RS + tt].x));
                         const float old = set_s[tt], x = md - ref_s[tt];
-                        float f = 1.f, del = 0.f;
+                        float f = 1.f;
                         if (x > old + 8.f) {
-                            del = -x - ref_s[tt];
-                            f = old == SC_NEG_INF ? 0.f : ex2(del);
+                            f = old == SC_NEG_INF ? 0.f : ex2(old - x);
                             set_s[tt] = x;
                             ref_s[tt] = -x;
                         }
                         fac_s[tt] = f;
-                        del_s[tt] = del;
                     }
                     unset = named_or(bar, 128, tt < NC && set_s[tt < NC ? tt : 0] == SC_NEG_INF);
+                    if (fresh) continue;
 #pragma unroll
                     for (int i = 0; i < NC; i += 2) {
                         const uint64_t f = *reinterpret_cast<const uint64_t*>(fac_s + i);
                         l[i / 2] = f2_mul(l[i / 2], f);
                         z[i / 2] = f2_mul(z[i / 2], f);
-                        d[i] += del_s[i];
-                        d[i + 1] += del_s[i + 1];
                     }
-                    if (!fresh && !failed) {
-                        if (!ALT && !tc_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, P.timeout_ns)) failed = true;
-                        tc_after();
-                        __syncwarp();
-                        if (o_mine) {
+                    if (!failed && !ALT && !sc_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, P.timeout_ns)) failed = true;
+                    tc_after();
+                    __syncwarp();
+                    if (o_mine && !failed) {
 #pragma unroll 1
-                            for (int g = 0; g < NC / 8; ++g) {
-                                float x[8];
-                                tc_ld8(o_addr + 8 * g, x);
-                                tc_wait_ld();
+                        for (int g = 0; g < NC; g += 8) {
+                            float x[8];
+                            tc_ld8(o_addr + g, x);
+                            tc_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] *= fac_s[8 * g + i];
-                                tc_st8(o_addr + 8 * g, x);
-                            }
-                            tc_wait_st();
+                            for (int i = 0; i < 8; ++i) x[i] *= fac_s[g + i];
+                            tc_st8(o_addr + g, x);
                         }
+                        tc_wait_st();
                     }
                 }
                 // ---- weights ----
@@ -900,11 +913,10 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                 const uint64_t vs2 = f2_pack(vs, vs), vz2 = f2_pack(vz, vz);
                 // bf16 codes count from 0 in the product: 8 of the rounded weight are taken off again,
                 // so that a weight's rounding meets code - 8 and not code
-                const float off = code ? v_off : 0.f;
                 const uint64_t off2 = f2_pack(off, off);
 #pragma unroll
                 for (int i = 0; i < NC; i += 2) {
-                    const uint64_t p2 = f2_pack(ex2(d[i]), ex2(d[i + 1]));
+                    const uint64_t p2 = f2_pack(p[i], p[i + 1]);
                     l[i / 2] = f2_add(l[i / 2], p2);
                     z[i / 2] = f2_fma(p2, vz2, z[i / 2]);
                     float s0, s1;
@@ -926,14 +938,13 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                 fence_async_smem();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) tc_arrive(&p_full[b]);
+                if (lane == 0) sc_arrive(&p_full[b]);
             }
             // ---- the segment's end: sums over the tokens, the two groups together, the output ----
-            const int tiles = it - it0;
-#pragma unroll
+#pragma unroll 1
             for (int k = 1; k <= 2; ++k)  // the last two products
-                if (tiles >= k && !failed && !tc_wait(&pv_done[(it - k) & 1], ((it - k) >> 1) & 1, P.timeout_ns)) failed = true;
-            if (dense && !failed && !tc_wait(&odd_full[dseg & 1], (dseg >> 1) & 1, P.timeout_ns)) failed = true;
+                if (tiles >= k && !failed && !sc_wait(&pv_done[(it - k) & 1], ((it - k) >> 1) & 1, P.timeout_ns)) failed = true;
+            if (dense && !failed && !sc_wait(&odd_full[dseg & 1], (dseg >> 1) & 1, P.timeout_ns)) failed = true;
             tc_after();
 #pragma unroll
             for (int g = 0; g < NC / 8; ++g) {
@@ -950,13 +961,13 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
             if (named_or(3, 256, failed)) failed = true;
             const bool whole = w.whole();
             const int slot = blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0);
-            constexpr int NO = N / 2;            // rows this group writes
-            const int c0 = half * NO;            // the first of them in the block
-            const int rw = (w.hr % P.row_blocks) * N + c0;
-            float* f0_s = reinterpret_cast<float*>(base + Sm::OFF_FAC);  // [ACC][N]: of the accumulators
-            float* z_s = reinterpret_cast<float*>(base + Sm::OFF_DEL);   // [N]
+            constexpr int NO = N / 2;  // rows this group writes
+            const int c0 = half * NO;  // the first of them in the block
+            float* f_s = reinterpret_cast<float*>(base + Sm::OFF_FAC) + c0;  // [ACC][N]: of the accumulators
+            float* z_s = reinterpret_cast<float*>(base + Sm::OFF_DEL) + c0;  // [N]
+            long long* at_s = reinterpret_cast<long long*>(base + Sm::OFF_AT) + c0;  // [N]: where a row goes, -1: nowhere
             if (tt < NO) {
-                const int col = c0 + tt;
+                const int col = c0 + tt, row = (w.hr % P.row_blocks) * N + col;
                 const float* sets = reinterpret_cast<const float*>(base + Sm::OFF_SET);
                 const float2* red = reinterpret_cast<const float2*>(base + Sm::OFF_RED);
                 float M = SC_NEG_INF, L = 0.f, Z = 0.f, wt[Sm::ACC];
@@ -965,7 +976,7 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
 #pragma unroll
                 for (int a = 0; a < Sm::ACC; ++a) {
                     float La = 0.f, Za = 0.f;
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < 4; ++i) {
                         const float2 v = red[i * RS + a * NC + col];
                         La += v.x;
@@ -973,46 +984,53 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                     }
                     const float m = sets[a * NC + col];
                     wt[a] = m == SC_NEG_INF ? 0.f : ex2(m - M);
-                    L += m == SC_NEG_INF ? La : La * wt[a];  // (without a reference the sum is 0 or NaN)
-                    Z += m == SC_NEG_INF ? Za : Za * wt[a];
+                    const float f = m == SC_NEG_INF ? 1.f : wt[a];  // (without a reference the sum is 0 or NaN)
+                    L = fmaf(La, f, L);
+                    Z = fmaf(Za, f, Z);
                 }
                 if (failed) L = nan;
+                // (a sum that is not a number makes its factors one, whatever was accumulated)
                 const float norm = L != L ? nan : !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-                for (int a = 0; a < Sm::ACC; ++a) f0_s[a * N + col] = wt[a] * norm * o_scale;
-                z_s[col] = Z * norm;
-                if (!whole)
+                for (int a = 0; a < Sm::ACC; ++a) f_s[a * N + tt] = wt[a] * norm * o_scale;
+                z_s[tt] = Z * norm;
+                long long at = -1;
+                if (!whole) {
                     P.part_ml[static_cast<size_t>(slot) * N + col] = make_float2(M, L);
-                else if (P.out_lse && rw + tt < P.rows)
-                    P.out_lse[sc_out_row(P, w.b, head, rw + tt)] = L == 0.f ? SC_NEG_INF : (M + log2f(L)) * SC_LN2;
+                    at = (static_cast<long long>(slot) * N + col) * D;
+                } else if (row < P.rows) {
+                    const size_t o = sc_out_row(P, w.b, head, row);
+                    if (P.out_lse) P.out_lse[o] = L == 0.f ? SC_NEG_INF : (M + log2f(L)) * SC_LN2;
+                    at = static_cast<long long>(o) * D;
+                }
+                at_s[tt] = at;
             }
             named_sync(bar, 128);
             if (o_mine) {
 #pragma unroll 1
-                for (int g = 0; g < NO / 8; ++g) {
+                for (int g = 0; g < NO; g += 8) {
                     float x[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] = 0.f;
-#pragma unroll
+#pragma unroll 1
                     for (int a = 0; a < Sm::ACC; ++a) {
                         // accumulator a was used by the part's tiles of its turn
                         if (!failed && tiles > 0 && (tiles > 1 || !ALT || (it0 & 1) == a)) {
                             float y[8];
-                            tc_ld8(tmem + Sm::T_O + a * N + c0 + 8 * g + lane_base, y);
+                            tc_ld8(tmem + Sm::T_O + a * N + c0 + g + lane_base, y);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], f0_s[a * N + c0 + 8 * g + i], x[i]);
+                            for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], f_s[a * N + g + i], x[i]);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        // (a sum that is not a number makes its factor one, whatever was accumulated)
-                        x[i] = fmaf(0.f, f0_s[c0 + 8 * g + i], x[i] + z_s[c0 + 8 * g + i]);
-                    }
+                    for (int i = 0; i < 8; ++i) x[i] = fmaf(0.f, f_s[g + i], x[i] + z_s[g + i]);
                     if (dense) {
                         const uint32_t* odd = odd_s + ((dseg & 1) * 4 + wq) * TC_MASK_WORDS;  // these 32 dims' warp
-                        const uint32_t* mask = reinterpret_cast<const uint32_t*>(base + Sm::OFF_MASK) + (c0 + 8 * g) * TC_MASK_WORDS;
+                        const uint32_t* mask = reinterpret_cast<const uint32_t*>(base + Sm::OFF_MASK) + (c0 + g) * TC_MASK_WORDS;
+#pragma unroll 1
                         for (int wd = 0; wd * 32 < P.n; ++wd)
+#pragma unroll 1
                             for (uint32_t m = odd[wd]; m; m &= m - 1) {
                                 const int j = wd * 32 + __ffs(m) - 1;
                                 const uint16_t e = reinterpret_cast<const uint16_t*>(P.v_new)
@@ -1027,12 +1045,11 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int row = rw + 8 * g + i;
+                        const long long at = at_s[g + i];
                         if (!whole)
-                            P.part_o[(static_cast<size_t>(slot) * N + c0 + 8 * g + i) * D + t] = x[i];
-                        else if (row < P.rows)
-                            static_cast<uint16_t*>(P.out)[sc_out_row(P, w.b, head, row) * D + t] =
-                                static_cast<uint16_t>(Ty::pack(x[i], 0.f));
+                            P.part_o[at + t] = x[i];
+                        else if (at >= 0)
+                            static_cast<uint16_t*>(P.out)[at + t] = static_cast<uint16_t>(Ty::pack(x[i], 0.f));
                     }
                 }
             }
@@ -1041,7 +1058,7 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
             named_sync(3, 256);  // the groups' statistics are free
             if (dense) ++dseg;
             if (act) {
-                if (lane == 0) tc_arrive(&q_empty[seg & 1]);
+                if (lane == 0) sc_arrive(&q_empty[seg & 1]);
                 ++seg;
             }
         }
@@ -1052,7 +1069,7 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
     __syncthreads();
     if (warp == 17) {
         // the MMAs of a CTA that stopped early may still be running: free tensor memory after them
-        if (!tc_wait(done, 0, P.timeout_ns)) *err_s = 1;
+        if (!sc_wait(done, 0, P.timeout_ns)) *err_s = 1;
         __syncwarp();
         tc_after();
         tc_dealloc(tmem, 512);

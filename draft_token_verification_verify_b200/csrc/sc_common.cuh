@@ -104,6 +104,70 @@ __device__ __forceinline__ uint32_t sc_center_f16(uint32_t x) {
     return r;
 }
 
+// A code in the low byte of a 16-bit float is its value times the smallest
+// subnormal (2^-133 in bf16, 2^-24 in fp16), exactly, and the tensor cores take
+// subnormals: a mask is the whole expansion.  In bf16 the second code of a byte
+// may stay four bits up (the exponent's lowest bit continues the mantissa
+// there), as 16 times its value: its other operand is divided by 16 instead.
+// Products come back into range by powers of two: the other operand is scaled
+// by 2^64 (2^60), the result by 2^69.
+// Pair j of a word's codes as 16-bit subnormals.  BF16: the odd pairs are 16
+// times their value.
+template <bool BF16>
+__device__ __forceinline__ uint32_t sc_codes(uint32_t w, uint32_t w8, int j) {
+    if constexpr (BF16)
+        return ((j & 2) ? w8 : w) & ((j & 1) ? 0x00F000F0u : 0x000F000Fu);
+    else
+        return (w >> (4 * j)) & 0x000F000Fu;
+}
+
+// The scalings that bring subnormal codes back into range: 2^64, 2^60, 2^69.
+constexpr float SC_2P64 = 18446744073709551616.f;
+constexpr float SC_2P60 = 1152921504606846976.f;
+constexpr float SC_2P69 = 590295810358705651712.f;
+
+__device__ __forceinline__ void sc_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Waits for phase `parity` of `bar`; false after about `limit_ns`.  A failed try
+// suspends the warp for a while before it looks at the clock.  The answer is the
+// warp's (a vote), which keeps the code behind it uniform.
+__device__ __forceinline__ bool sc_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) return false;
+    }
+}
+
+// fp32 pairs
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // m16n8k16 on the tensor cores, fp32 accumulators.
 template <int DT>
 __device__ __forceinline__ void sc_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

@@ -9,6 +9,7 @@ struct AttendKernel {
     void (*fn)(AttendParams);
     int threads, smem;  // of a CTA
     int block_rows;     // rows a CTA takes at once
+    int per_sm;         // CTAs an SM holds
 };
 
 constexpr int SC_MOST_ROWS = 80;  // of a block

@@ -107,7 +107,7 @@ bool make_plan(const DeviceInfo& d, int B, int n, int q_heads, int kv_heads, int
     if (rows > (1 << 24)) return false;
     p->k = pick_attend(dt, D, static_cast<int>(ceil_div(rows, ceil_div(rows, sv::SC_MOST_ROWS))));
     p->row_blocks = static_cast<int>(ceil_div(rows, p->k.block_rows));
-    p->grid = d.sms;
+    p->grid = p->k.per_sm * d.sms;
     const size_t parts = static_cast<size_t>(p->grid) * 2 * p->k.block_rows;
     p->off_ml = round_up(parts * D * sizeof(float), 256);
     p->off_desc = p->off_ml + round_up(parts * sizeof(float2), 256);
