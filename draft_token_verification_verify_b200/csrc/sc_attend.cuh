@@ -190,8 +190,9 @@ struct AttendSmem {
     static constexpr int MERGE_ROW = D + 4;  // floats
     static constexpr int MERGE = SC_ROWS * MERGE_ROW * 4;  // a warp's output, or its staged value rows
     static constexpr int OFF_ML = RING + SC_WARPS * MERGE;
-    static constexpr int OFF_BAD = OFF_ML + SC_WARPS * SC_ROWS * 8;  // int [GROUPS][STAGES]
-    static constexpr int OFF_BAR = OFF_BAD + GROUPS * STAGES * 4;
+    static constexpr int OFF_PAR = OFF_ML + SC_WARPS * SC_ROWS * 8;  // float [warps][32 token pairs][8]
+    static constexpr int OFF_BAD = OFF_PAR + SC_WARPS * 1024;        // int [GROUPS][16]: segments with a bad page
+    static constexpr int OFF_BAR = OFF_BAD + GROUPS * 64;
     static constexpr int BYTES = OFF_BAR + 2 * GROUPS * STAGES * 8;
     static_assert(SC_ROWS * (D + 8) * 2 <= MERGE, "staged value rows fit the merge buffer");
     static_assert(OFF_BAR % 8 == 0 && 2 * (BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -215,7 +216,8 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     unsigned char* ring = sc_raw + group * STAGES * Sm::TILE;
     float* merge = reinterpret_cast<float*>(sc_raw + Sm::RING + warp * Sm::MERGE);
     float2* ml = reinterpret_cast<float2*>(sc_raw + Sm::OFF_ML);
-    volatile int* bad_s = reinterpret_cast<int*>(sc_raw + Sm::OFF_BAD) + group * STAGES;
+    ulonglong2* par_s = reinterpret_cast<ulonglong2*>(sc_raw + Sm::OFF_PAR + warp * 1024);
+    volatile int* bad_s = reinterpret_cast<int*>(sc_raw + Sm::OFF_BAD) + group * 16;
     uint64_t* full = reinterpret_cast<uint64_t*>(sc_raw + Sm::OFF_BAR) + group * STAGES;
     uint64_t* empty = full + G * STAGES;  // (MB > 1: the group's warps have read a stage)
     const CacheView& c = P.c;
@@ -233,6 +235,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         }
         fence_mbar_init();
     }
+    if (mb == 0 && lane < 16) bad_s[lane] = 0;
     __syncthreads();
 
     const int nb = SC_BLOCK >> c.log2_block;  // blocks of a tile
@@ -241,25 +244,36 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     const float sl = P.scale * SC_LOG2E;
 
     // ---- the copies of a group, by its first warp: STAGES tiles ahead ----
+    const size_t block_bytes = 2 * sc_half_bytes<D>(c.block);
+    const size_t head_bytes = block_bytes * (c.page_size >> c.log2_block), page_bytes = head_bytes * c.kv_heads;
     Walk<SC_BLOCK> iw;
     iw.begin(P, R);
     iw.u = iw.u0 + group;
     bool more = true;
-    int ahead_id = 0, ahead_sub = 0;
-    auto settle = [&]() {  // to the next cache tile at or behind iw.u
-#pragma unroll 1
-        while (more) {
-            if (iw.u < iw.u1 && iw.u * SC_BLOCK < iw.len) break;
-            more = iw.next(P);
-            iw.u = iw.u0 + group;
-        }
-        if (more && lane < nb) {  // lane j fetches block j of the tile
-            const int t = iw.u * SC_BLOCK + (lane << c.log2_block);
-            ahead_id = t < iw.len ? __ldg(c.table + static_cast<size_t>(iw.b) * c.max_pages + (t >> c.log2_page)) : -2;
-            ahead_sub = (t & (c.page_size - 1)) >> c.log2_block;
-        }
+    int iw_end = 0, iw_seg = 0;  // behind the part's cache tiles; segments so far
+    int ahead_id = 0, issued = 0, used = 0;
+    const unsigned char* ahead = nullptr;  // the tile's first block on a page at 0
+    const int32_t* table = nullptr;
+    auto part = [&]() {  // the walk has entered a part
+        const int tiles = (iw.len + SC_BLOCK - 1) / SC_BLOCK;
+        iw_end = iw.u1 < tiles ? iw.u1 : tiles;
+        table = c.table + static_cast<size_t>(iw.b) * c.max_pages;
+        ahead = c.pages + head_bytes * (iw.hr / P.row_blocks);
     };
-    int issued = 0, used = 0;
+    part();
+    // Fetches the page of the next cache tile (at or behind iw.u); lane j that of
+    // its block j.  Nothing looks at it before the next copy: its latency is hidden.
+    auto fetch = [&]() {
+#pragma unroll 1
+        while (iw.u >= iw_end) {
+            if (!(more = iw.next(P))) return;
+            ++iw_seg;
+            iw.u = iw.u0 + group;
+            part();
+        }
+        const int t = iw.u * SC_BLOCK + (lane << c.log2_block);
+        ahead_id = __ldg(table + ((lane < nb && t < iw.len ? t : iw.u * SC_BLOCK) >> c.log2_page));
+    };
     auto issue = [&]() {
         if (!more || error) return;
         const int s = issued % STAGES;
@@ -267,41 +281,53 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
             error = true;
             return;
         }
-        const bool mine = lane < nb && ahead_id != -2;
-        const bool ok = mine && ahead_id >= 0 && ahead_id < c.num_pages && !P.test_hook;
-        const unsigned got = __ballot_sync(ALL, ok), want = __ballot_sync(ALL, mine);
-        if (lane == 0) {
-            bad_s[s] = got != want && !P.test_hook;
-            mbar_arrive_expect_tx(&full[s], P.test_hook ? bbytes : bbytes * __popc(got));
+        unsigned char* dst = ring + s * Sm::TILE;
+        if (nb == 1) {
+            const int id = __shfl_sync(ALL, ahead_id, 0);
+            const bool fine = static_cast<unsigned>(id) < static_cast<unsigned>(c.num_pages);
+            if (sc_elect()) {
+                if (!fine) bad_s[iw_seg & 15] = 1;
+                mbar_arrive_expect_tx(&full[s], fine || P.test_hook ? bbytes : 0u);
+                if (fine && !P.test_hook)
+                    bulk_g2s(dst, ahead + page_bytes * id + block_bytes * ((iw.u * SC_BLOCK & (c.page_size - 1)) / SC_BLOCK),
+                             bbytes, &full[s]);
+            }
+        } else {
+            const bool mine = lane < nb && iw.u * SC_BLOCK + (lane << c.log2_block) < iw.len;
+            const bool fine = mine && static_cast<unsigned>(ahead_id) < static_cast<unsigned>(c.num_pages);
+            const unsigned got = __ballot_sync(ALL, fine), want = __ballot_sync(ALL, mine);
+            if (lane == 0) {
+                if (got != want) bad_s[iw_seg & 15] = 1;
+                mbar_arrive_expect_tx(&full[s], bbytes * (P.test_hook ? 1 : __popc(got)));
+            }
+            __syncwarp();
+            if (fine && !P.test_hook) bulk_g2s(dst + lane * bstride, ahead + page_bytes * ahead_id, bbytes, &full[s]);
         }
         __syncwarp();
-        if (ok)
-            bulk_g2s(ring + s * Sm::TILE + lane * bstride, sc_block_ptr<D>(c, ahead_id, iw.hr / P.row_blocks, ahead_sub),
-                     bbytes, &full[s]);
         ++issued;
         iw.u += G;
-        settle();
+        fetch();
     };
     if (mb == 0) {
-        settle();
+        fetch();
 #pragma unroll 1
         for (int s = 0; s < (MB == 1 ? STAGES : STAGES - 1); ++s) issue();
     }
 
-    // Token 2 t + i of a lane's 16: what its code's product and its weight are
-    // multiplied by (even and odd t).
+    // What a code's product and a weight are multiplied by.
     const float k_code = DT == 0 ? SC_2P69 : 16777216.f;
-    const uint64_t v_even = DT == 0 ? f2_pack(SC_2P64, SC_2P64) : f2_pack(1.f, 1.f);
-    const uint64_t v_odd = DT == 0 ? f2_pack(SC_2P60, SC_2P60) : v_even;
+    const float v1 = lane & 1 ? SC_2P60 : SC_2P64;  // of the weights of tokens 2 lane, 2 lane + 1
+    const uint64_t v_code = f2_pack(v1, v1);
     const uint64_t kc2 = f2_pack(sl * k_code, sl * k_code), sl2 = f2_pack(sl, sl), eight2 = f2_pack(8.f, 8.f);
     // this lane's shares of a tile: its key rows, its 16 tokens' parameters, its value rows
     const int tk = 16 * (r8 >> 1), tq = 16 * q4, Tb = c.block;
     const uint32_t k_off = (tk >> c.log2_block) * bstride + ((tk & (Tb - 1)) + (r8 & 1)) * (D / 2) + q4 * (D / 8);
     const uint32_t q_blk = (tq >> c.log2_block) * bstride;
-    const uint32_t p_off = q_blk + Tb * (D / 2) + (tq & (Tb - 1)) * 4;
+    const uint32_t l_off = ((2 * lane) >> c.log2_block) * bstride + Tb * (D / 2) + ((2 * lane) & (Tb - 1)) * 4;
     const uint32_t v_off = q_blk + sc_half_bytes<D>(Tb) + r8 * (Tb / 2) + (tq & (Tb - 1)) / 2;
     const uint32_t half_bytes = sc_half_bytes<D>(Tb), v_step = 8 * (Tb / 2);
 
+    int seg = 0;  // segments so far
     Walk<SC_BLOCK> w;
     w.begin(P, R);
 #pragma unroll 1
@@ -389,12 +415,33 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                 // ---- a tile of 64 cached tokens ----
                 if (MB > 1 && mb == 0) issue();  // into the stage of the tile before this one
                 const int s = used % STAGES;
-                if (!error) error = !sc_wait(&full[s], (used / STAGES) & 1, P.timeout_ns);
-                if (error || __any_sync(ALL, bad_s[s])) poison();
-                if (error) continue;  // nothing more is waited for
+                if (error || !sc_wait(&full[s], (used / STAGES) & 1, P.timeout_ns)) {
+                    error = true;  // nothing more is waited for
+                    poison();
+                    continue;
+                }
                 ++used;
                 const int valid = w.len - u * SC_BLOCK;
                 const unsigned char* tile = ring + s * Sm::TILE;
+                // lane l prepares the parameters of the tokens 2 l, 2 l + 1 for the warp: of a score,
+                // scale and zero; of a weight, the value's scale and its middle (codes count from 8)
+                {
+                    const uint2 kp = *reinterpret_cast<const uint2*>(tile + l_off);
+                    uint2 vp = *reinterpret_cast<const uint2*>(tile + l_off + half_bytes);
+                    if (valid < SC_BLOCK) {  // what lies behind the last token may be anything
+                        if (2 * lane >= valid) vp.x = 0u;
+                        if (2 * lane + 1 >= valid) vp.y = 0u;
+                    }
+                    const uint64_t s2 = f2_pack(Ty::lo(vp.x), Ty::lo(vp.y));
+                    ulonglong2 y;
+                    y.x = f2_mul(f2_pack(Ty::lo(kp.x), Ty::lo(kp.y)), kc2);
+                    y.y = f2_mul(f2_pack(Ty::hi(kp.x), Ty::hi(kp.y)), sl2);
+                    par_s[2 * lane] = y;
+                    y.x = DT == 0 ? f2_mul(s2, v_code) : s2;
+                    y.y = f2_fma(s2, eight2, f2_pack(Ty::hi(vp.x), Ty::hi(vp.y)));
+                    par_s[2 * lane + 1] = y;
+                    __syncwarp();
+                }
                 // scores: lane r8 of n-tile t takes token 16 (r8 / 2) + 2 t + r8 % 2, so that
                 // the accumulators of a lane are the 16 tokens 16 q4 .. 16 q4 + 15
                 float x[8][4];
@@ -417,28 +464,24 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < KS; k += 2)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t wd = kw[i][k >> 1], w8 = wd >> 8;
-                            sc_mma<DT>(x[t4 + i], qa[k], sc_codes<DT == 0>(wd, w8, 0), sc_codes<DT == 0>(wd, w8, 1));
-                            sc_mma<DT>(x[t4 + i], qa[k + 1], sc_codes<DT == 0>(wd, w8, 2), sc_codes<DT == 0>(wd, w8, 3));
-                        }
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t wd = kw[i][k >> 1], w8 = wd >> 8;
+                                sc_mma<DT>(x[t4 + i], qa[k + j], sc_codes<DT == 0>(wd, w8, 2 * j),
+                                           sc_codes<DT == 0>(wd, w8, 2 * j + 1));
+                            }
                 }
                 // relative to the reference: scale (q . code) + zero sum(q) - reference
                 const uint64_t q2[2] = {f2_pack(qs[0], qs[0]), f2_pack(qs[1], qs[1])};
                 const uint64_t n2[2] = {f2_pack(nref[0], nref[0]), f2_pack(nref[1], nref[1])};
 #pragma unroll
-                for (int t = 0; t < 8; t += 2) {
-                    const uint4 pr = *reinterpret_cast<const uint4*>(tile + p_off + t * 8);
-                    const uint32_t pw[4] = {pr.x, pr.y, pr.z, pr.w};
+                for (int t = 0; t < 8; ++t) {
+                    const ulonglong2 y = par_s[2 * (8 * q4 + t)];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t a2 = f2_mul(f2_pack(Ty::lo(pw[2 * h]), Ty::lo(pw[2 * h + 1])), kc2);
-                        const uint64_t b2 = f2_mul(f2_pack(Ty::hi(pw[2 * h]), Ty::hi(pw[2 * h + 1])), sl2);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float* d = &x[t + h][2 * e];
-                            f2_unpack(f2_fma(a2, f2_pack(d[0], d[1]), f2_fma(b2, q2[e], n2[e])), d[0], d[1]);
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        float* d = &x[t][2 * e];
+                        f2_unpack(f2_fma(y.x, f2_pack(d[0], d[1]), f2_fma(y.y, q2[e], n2[e])), d[0], d[1]);
                     }
                 }
                 if (valid < SC_BLOCK) {
@@ -465,35 +508,23 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                 // softmax weights times the values' scales
                 uint32_t pa[4][4], pl[4][4];
 #pragma unroll
-                for (int t = 0; t < 8; t += 2) {
-                    const uint4 pr = *reinterpret_cast<const uint4*>(tile + p_off + half_bytes + t * 8);
-                    uint32_t pw[4] = {pr.x, pr.y, pr.z, pr.w};
-                    if (valid < SC_BLOCK) {  // what lies behind the last token may be anything
+                for (int t = 0; t < 8; ++t) {
+                    const ulonglong2 y = par_s[2 * (8 * q4 + t) + 1];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (tq + 2 * t + i >= valid) pw[i] = 0u;
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t s2 = f2_pack(Ty::lo(pw[2 * h]), Ty::lo(pw[2 * h + 1]));
-                        // the values' middle: codes count from 8
-                        const uint64_t z2 = f2_fma(s2, eight2, f2_pack(Ty::hi(pw[2 * h]), Ty::hi(pw[2 * h + 1])));
-                        const uint64_t sv2 = DT == 0 ? f2_mul(s2, h ? v_odd : v_even) : s2;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint64_t p2 = f2_pack(ex2(x[t + h][2 * e]), ex2(x[t + h][2 * e + 1]));
-                            l[e] = f2_add(l[e], p2);
-                            z[e] = f2_fma(p2, z2, z[e]);
-                            float s0, s1;
-                            f2_unpack(f2_mul(p2, sv2), s0, s1);
-                            // rounded to bf16 whatever the cache's type: p * scale keeps fp32's range there;
-                            // with fp16 activations the rest goes through the product as well
-                            const uint32_t hi = SC<0>::pack(s0, s1);
-                            pa[t >> 1][2 * h + e] = hi;
-                            if constexpr (DT == 1) pl[t >> 1][2 * h + e] = SC<0>::pack(s0 - SC<0>::lo(hi), s1 - SC<0>::hi(hi));
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        const uint64_t p2 = f2_pack(ex2(x[t][2 * e]), ex2(x[t][2 * e + 1]));
+                        l[e] = f2_add(l[e], p2);
+                        z[e] = f2_fma(p2, y.y, z[e]);
+                        float s0, s1;
+                        f2_unpack(f2_mul(p2, y.x), s0, s1);
+                        // rounded to bf16 whatever the cache's type: p * scale keeps fp32's range there;
+                        // with fp16 activations the rest goes through the product as well
+                        const uint32_t hi = SC<0>::pack(s0, s1);
+                        pa[t >> 1][2 * (t & 1) + e] = hi;
+                        if constexpr (DT == 1) pl[t >> 1][2 * (t & 1) + e] = SC<0>::pack(s0 - SC<0>::lo(hi), s1 - SC<0>::hi(hi));
                     }
                 }
+                __syncwarp();
 #pragma unroll
                 for (int u4 = 0; u4 < NV; u4 += 4) {
                     uint2 vw[4];
@@ -501,20 +532,17 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                     for (int i = 0; i < 4; ++i)
                         vw[i] = *reinterpret_cast<const uint2*>(tile + v_off + (u4 + i) * v_step);
 #pragma unroll
-                    for (int k = 0; k < 4; k += 2)
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t wd = k ? vw[i].y : vw[i].x, w8 = wd >> 8;
-                            uint32_t vb[4];
+                            const uint32_t wd = k < 2 ? vw[i].x : vw[i].y, w8 = wd >> 8;
+                            uint32_t vb[2];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                vb[j] = DT == 0 ? sc_codes<true>(wd, w8, j) : sc_center_bf16(sc_codes_bf16(wd, j));
+                            for (int j = 0; j < 2; ++j)
+                                vb[j] = DT == 0 ? sc_codes<true>(wd, w8, 2 * (k & 1) + j)
+                                                : sc_center_bf16(sc_codes_bf16(wd, 2 * (k & 1) + j));
                             sc_mma<0>(o[u4 + i], pa[k], vb[0], vb[1]);
-                            sc_mma<0>(o[u4 + i], pa[k + 1], vb[2], vb[3]);
-                            if constexpr (DT == 1) {
-                                sc_mma<0>(o[u4 + i], pl[k], vb[0], vb[1]);
-                                sc_mma<0>(o[u4 + i], pl[k + 1], vb[2], vb[3]);
-                            }
+                            if constexpr (DT == 1) sc_mma<0>(o[u4 + i], pl[k], vb[0], vb[1]);
                         }
                 }
                 // bf16 codes count from 0 in the product: 8 of the rounded weights are summed beside
@@ -686,6 +714,8 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
             }
         }
 
+        if (__any_sync(ALL, bad_s[seg & 15])) poison();  // a page out of range
+        ++seg;
         // ---- merge the groups: 16 rows of (reference, sum, output) a warp ----
         const float os = DT == 0 ? SC_2P69 : 1.f;
 #pragma unroll
@@ -756,6 +786,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         }
         if (tid == 0 && w.u0 == 0 && !whole)
             P.desc[blockIdx.x] = make_int4(w.b, w.hr, w.parts(static_cast<int>(R.chunk)), 0);
+        if (mb == 0 && lane == 0) bad_s[(seg - 1) & 15] = 0;
         __syncthreads();  // the merge buffers are free
     }
     // no copy may land after the CTA is gone (after an error some are still under way)

@@ -128,11 +128,6 @@ __device__ __forceinline__ bool tc_test(uint64_t* bar, uint32_t parity) {
         : "memory");
     return __all_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
 // Registers of a group of four warps.  The CTA starts with 640 x 96 = 61,440;
 // 128 x (56 + 72 + 72 + 2 x 136) = 60,416 are given out.
 template <int R>
@@ -353,7 +348,7 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
         // ---- the MMAs: whichever product has its operands, O first; the warp stays
         // together and one elected lane issues, so that the operands are uniform ----
         constexpr uint32_t id_qk = tc_idesc(DT == 0, N), id_pv = tc_idesc(1, N);
-        const bool leader = elect_one();
+        const bool leader = sc_elect();
         const uint64_t q_desc = tc_desc(smem_u32(base)), p_desc = tc_desc(smem_u32(base + Sm::OFF_P));
         int qi = 0, pi = 0;              // the next tile's S, and O
         uint32_t firsts = 0, denses = 0;  // bit i & 31: of tile i
