@@ -9,9 +9,7 @@ the call (TypeError / ValueError).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import math
 import os
 from typing import Optional
 
@@ -131,6 +129,10 @@ class KvCache:
         self.pages, self.head_dim, self.dtype = pages, int(head_dim), dtype
         self.num_pages, self.kv_heads, self.page_size = pages.shape[0], pages.shape[1], size
         self.device = pages.device
+        code = SV_DTYPE_F16 if dtype == torch.float16 else 0
+        self._struct = SvCache(pages.data_ptr(), None, None, self.num_pages, 0, size, self.kv_heads, self.head_dim, code)
+        self._index = pages.get_device()
+        self._workspace = {}  # bytes by (B, n, q_heads)
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=None, device="cuda"):
@@ -143,86 +145,96 @@ class KvCache:
     def struct(self, page_table, lens) -> SvCache:
         """``sv_cache_t`` of the pages with one batch's page table [B, max_pages]
         and lengths [B] (int32).  Keep the tensors alive until the call completes."""
-        import torch
+        c = SvCache.from_buffer_copy(self._struct)
+        c.page_table, c.lens, c.max_pages = page_table.data_ptr(), lens.data_ptr(), page_table.shape[1]
+        return c
 
-        code = SV_DTYPE_F16 if self.dtype == torch.float16 else 0
-        return SvCache(self.pages.data_ptr(), page_table.data_ptr(), lens.data_ptr(), self.num_pages,
-                       page_table.shape[1], self.page_size, self.kv_heads, self.head_dim, code)
+    def workspace_bytes(self, B: int, n: int, q_heads: int) -> int:
+        """Workspace of ``cache_attend`` for these sizes on the current device."""
+        need = self._workspace.get((B, n, q_heads))
+        if need is None:
+            need = spec_cache_attend_workspace_size(B, n, q_heads, self.kv_heads, self.head_dim)
+            if need == 0:
+                _fail(-2, "spec_cache_attend_workspace_size")
+            self._workspace[B, n, q_heads] = need
+        return need
 
 
-def _ints(t, name, shape, device):
+def _ints(t, name, shape, cache):
+    """Checks a contiguous int32 tensor of `shape` on the pages' device."""
     import torch
 
-    if not hasattr(t, "data_ptr"):
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the pages on {device}")
+    if t.get_device() != cache._index:
+        raise ValueError(f"{name} is on {t.device}, the pages on {cache.device}")
 
 
 def _tokens(t, name, cache, heads=None):
     """Checks activations [B, n, heads, D] whose heads lie side by side and
     whose tokens are evenly spaced (a part of a fused projection's rows will
-    do); returns the elements between tokens."""
-    if not hasattr(t, "data_ptr"):
+    do); returns (shape, elements between tokens)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != cache.dtype:
+    if t.dtype is not cache.dtype:
         raise TypeError(f"{name} must be {cache.dtype} like the cache, got {t.dtype}")
-    if t.dim() != 4 or t.shape[3] != cache.head_dim or (heads is not None and t.shape[2] != heads) or t.numel() == 0:
-        raise ValueError(f"{name} must be [B, n, {heads or 'heads'}, {cache.head_dim}], got shape {tuple(t.shape)}")
-    if t.device != cache.device:
+    shape = t.shape
+    if len(shape) != 4 or shape[3] != cache.head_dim or (heads is not None and shape[2] != heads) or 0 in shape:
+        raise ValueError(f"{name} must be [B, n, {heads or 'heads'}, {cache.head_dim}], got shape {tuple(shape)}")
+    if t.get_device() != cache._index:
         raise ValueError(f"{name} is on {t.device}, the pages on {cache.device}")
-    (B, n, H, D), (sb, sn, sh, sd) = t.shape, t.stride()
+    B, n, H, D = shape
+    sb, sn, sh, sd = t.stride()
     step = sn if n > 1 else sb if B > 1 else H * D
     if sd != 1 or (H > 1 and sh != D) or (n > 1 and B > 1 and sb != n * sn) or step < H * D:
         raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, got strides {t.stride()}")
     if step % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name}: tokens must be 16-byte aligned")
-    return step
+    return shape, step
+
+
+def _out(t, name, dtype, shape, cache):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != cache._index:
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {cache.device}")
 
 
 def _batch(cache, page_table, lens, B):
+    """Checks the page table and lengths of B sequences."""
     import torch
 
     if not isinstance(cache, KvCache):
         raise TypeError("cache must be a KvCache")
-    if cache.device.type != "cuda":
+    if cache._index < 0:
         raise ValueError(f"tensors must be on a CUDA device, got {cache.device}")
-    _ints(lens, "lens", (B,), cache.device)
-    if not hasattr(page_table, "data_ptr") or page_table.dim() != 2 or page_table.shape[1] < 1:
+    _ints(lens, "lens", (B,), cache)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[1] < 1:
         raise ValueError("page_table must be a [B, max_pages] tensor")
-    _ints(page_table, "page_table", (B, page_table.shape[1]), cache.device)
+    _ints(page_table, "page_table", (B, page_table.shape[1]), cache)
 
 
-@contextlib.contextmanager
-def _nested(*managers):
-    with contextlib.ExitStack() as stack:
-        for m in managers:
-            stack.enter_context(m)
-        yield
-
-
-def _on(device, stream):
-    """(context, raw stream): the pages' device is made current where it is
-    not, and what the call allocates belongs to the stream it runs on."""
+def _on(cache, stream, call):
+    """Runs ``call(raw stream)`` with the pages' device current and what it
+    allocates belonging to the stream it runs on."""
     import torch
 
-    managers = []
-    if device.index is not None and device.index != torch.cuda.current_device():
-        managers.append(torch.cuda.device(device))
+    # (torch.cuda's own functions of these names cost several times the launch)
+    if torch._C._cuda_getDevice() != cache._index:
+        with torch.cuda.device(cache._index):
+            return _on(cache, stream, call)
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
-    else:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        raw = stream.cuda_stream
-        managers.append(torch.cuda.stream(stream))
-    return (_nested(*managers) if managers else contextlib.nullcontext()), raw
+        return call(torch._C._cuda_getCurrentRawStream(cache._index))
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=cache.device)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def cache_attend(q, cache: KvCache, page_table, lens, k=None, v=None, parents=None, scale: Optional[float] = None,
@@ -238,56 +250,51 @@ def cache_attend(q, cache: KvCache, page_table, lens, k=None, v=None, parents=No
     that can overlap need one each).  Returns out."""
     import torch
 
-    B, n = q.shape[:2] if hasattr(q, "data_ptr") and q.dim() == 4 else (0, 0)
+    if not isinstance(cache, KvCache):
+        raise TypeError("cache must be a KvCache")
+    (B, n, Hq, D), q_step = _tokens(q, "q", cache)
     _batch(cache, page_table, lens, B)
-    dev, D = cache.device, cache.head_dim
-    q_step = _tokens(q, "q", cache)
-    Hq = q.shape[2]
+    dev = cache.device
     if Hq % cache.kv_heads:
         raise ValueError(f"{Hq} query heads are no multiple of {cache.kv_heads} key/value heads")
     if n > 257:
         raise ValueError(f"at most 257 positions per sequence, got {n}")
     if (k is None) != (v is None):
         raise ValueError("k and v come together")
+    k_ptr = v_ptr = None
     kv_step = 0
     if k is not None:
-        kv_step = _tokens(k, "k", cache, cache.kv_heads)
-        if k.shape[:2] != (B, n) or v.shape[:2] != (B, n):
-            raise ValueError(f"k and v must have the tokens of q: {tuple(k.shape)}, {tuple(v.shape)}")
-        if _tokens(v, "v", cache, cache.kv_heads) != kv_step:
+        shape, kv_step = _tokens(k, "k", cache, cache.kv_heads)
+        v_shape, v_step = _tokens(v, "v", cache, cache.kv_heads)
+        if shape[0] != B or shape[1] != n or v_shape != shape:
+            raise ValueError(f"k and v must have the tokens of q: {tuple(shape)}, {tuple(v_shape)}")
+        if v_step != kv_step:
             raise ValueError("k and v must have the same strides")
+        k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
     if parents is not None:
-        _ints(parents, "parents", (B, n - 1), dev)
+        _ints(parents, "parents", (B, n - 1), cache)
     if out is not None:
-        if out.dtype != cache.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
-            raise ValueError(f"out must be contiguous {cache.dtype} {list(q.shape)} on {dev}")
+        _out(out, "out", cache.dtype, q.shape, cache)
     if out_lse is not None:
-        if out_lse.dtype != torch.float32 or out_lse.shape != (B, n, Hq) or not out_lse.is_contiguous() or \
-                out_lse.device != dev:
-            raise ValueError(f"out_lse must be contiguous torch.float32 {[B, n, Hq]} on {dev}")
+        _out(out_lse, "out_lse", torch.float32, (B, n, Hq), cache)
     if out_status is not None:
-        _ints(out_status, "out_status", (1,), dev)
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        _ints(out_status, "out_status", (1,), cache)
+    if workspace is not None and (workspace.get_device() != cache._index or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be contiguous on {dev}")
-    context, raw = _on(dev, stream)
-    with context:
-        if out is None:
-            out = torch.empty((B, n, Hq, D), dtype=cache.dtype, device=dev)
-        if workspace is None:
-            need = cache_lib().spec_cache_attend_workspace_size(B, n, Hq, cache.kv_heads, D)
-            if need == 0:
-                _fail(-2, "spec_cache_attend_workspace_size")
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+
+    def call(raw):
+        o = q.new_empty((B, n, Hq, D)) if out is None else out
+        ws = cache.pages.new_empty(cache.workspace_bytes(B, n, Hq)) if workspace is None else workspace
         st = cache_lib().spec_cache_attend(
-            q.data_ptr(), q_step, None if k is None else k.data_ptr(), None if v is None else v.data_ptr(), kv_step,
-            None if parents is None or n == 1 else parents.data_ptr(), ctypes.byref(cache.struct(page_table, lens)),
-            B, n, Hq, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(),
-            None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), None if opts is None else ctypes.byref(opts),
-            None if out_status is None else out_status.data_ptr(), raw)
-    if st != 0:
-        _fail(st, "spec_cache_attend")
-    return out
+            q.data_ptr(), q_step, k_ptr, v_ptr, kv_step, None if parents is None or n == 1 else parents.data_ptr(),
+            ctypes.byref(cache.struct(page_table, lens)), B, n, Hq, D ** -0.5 if scale is None else scale, o.data_ptr(),
+            None if out_lse is None else out_lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+            None if opts is None else ctypes.byref(opts), None if out_status is None else out_status.data_ptr(), raw)
+        if st != 0:
+            _fail(st, "spec_cache_attend")
+        return o
+
+    return _on(cache, stream, call)
 
 
 def cache_append(cache: KvCache, page_table, lens, k, v, n_accepted=None, nodes=None, out_lens=None, stream=None):
@@ -300,33 +307,36 @@ def cache_append(cache: KvCache, page_table, lens, k, v, n_accepted=None, nodes=
     Returns the new lengths (-1: a data error of that sequence)."""
     import torch
 
-    B, n = k.shape[:2] if hasattr(k, "data_ptr") and k.dim() == 4 else (0, 0)
+    if not isinstance(cache, KvCache):
+        raise TypeError("cache must be a KvCache")
+    shape, step = _tokens(k, "k", cache, cache.kv_heads)
+    B, n = shape[0], shape[1]
     _batch(cache, page_table, lens, B)
-    dev = cache.device
-    step = _tokens(k, "k", cache, cache.kv_heads)
-    if _tokens(v, "v", cache, cache.kv_heads) != step or v.shape != k.shape:
-        raise ValueError(f"v must have the shape and strides of k: {tuple(v.shape)}, {tuple(k.shape)}")
+    v_shape, v_step = _tokens(v, "v", cache, cache.kv_heads)
+    if v_shape != shape or v_step != step:
+        raise ValueError(f"v must have the shape and strides of k: {tuple(v_shape)}, {tuple(shape)}")
     if n_accepted is not None:
-        _ints(n_accepted, "n_accepted", (B,), dev)
+        _ints(n_accepted, "n_accepted", (B,), cache)
     stride = 0
     if nodes is not None:
-        if not hasattr(nodes, "data_ptr") or nodes.dim() != 2 or nodes.shape[1] < n - 1:
+        if not isinstance(nodes, torch.Tensor) or nodes.dim() != 2 or nodes.shape[1] < n - 1:
             raise ValueError(f"nodes must be [B, >= {n - 1}]")
-        _ints(nodes, "nodes", (B, nodes.shape[1]), dev)
         stride = nodes.shape[1]
+        _ints(nodes, "nodes", (B, stride), cache)
     if out_lens is not None:
-        _ints(out_lens, "out_lens", (B,), dev)
-    context, raw = _on(dev, stream)
-    with context:
-        if out_lens is None:
-            out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        _ints(out_lens, "out_lens", (B,), cache)
+
+    def call(raw):
+        new = lens.new_empty(B) if out_lens is None else out_lens
         st = cache_lib().spec_cache_append(
             ctypes.byref(cache.struct(page_table, lens)), k.data_ptr(), v.data_ptr(), step, B, n,
-            None if n_accepted is None else n_accepted.data_ptr(),
-            None if nodes is None or stride == 0 else nodes.data_ptr(), stride, out_lens.data_ptr(), raw)
-    if st != 0:
-        _fail(st, "spec_cache_append")
-    return out_lens
+            None if n_accepted is None else n_accepted.data_ptr(), nodes.data_ptr() if stride else None, stride,
+            new.data_ptr(), raw)
+        if st != 0:
+            _fail(st, "spec_cache_append")
+        return new
+
+    return _on(cache, stream, call)
 
 
 def cache_read(cache: KvCache, page_table, lens, n: int, first=None, out_k=None, out_v=None, stream=None):
@@ -335,26 +345,27 @@ def cache_read(cache: KvCache, page_table, lens, n: int, first=None, out_k=None,
     rows outside a sequence's ``lens`` tokens are zeros."""
     import torch
 
-    B = lens.shape[0] if hasattr(lens, "data_ptr") and lens.dim() == 1 else 0
+    if not isinstance(lens, torch.Tensor) or lens.dim() != 1:
+        raise ValueError("lens must be a [B] tensor")
+    B = lens.shape[0]
     _batch(cache, page_table, lens, B)
-    dev = cache.device
     if n < 1 or B < 1:
         raise ValueError("nothing to read")
     if first is not None:
-        _ints(first, "first", (B,), dev)
+        _ints(first, "first", (B,), cache)
     shape = (B, n, cache.kv_heads, cache.head_dim)
-    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
-        if t is not None and (t.dtype != cache.dtype or t.shape != shape or not t.is_contiguous() or t.device != dev):
-            raise ValueError(f"{name} must be contiguous {cache.dtype} {list(shape)} on {dev}")
-    context, raw = _on(dev, stream)
-    with context:
-        if out_k is None:
-            out_k = torch.empty(shape, dtype=cache.dtype, device=dev)
-        if out_v is None:
-            out_v = torch.empty(shape, dtype=cache.dtype, device=dev)
+    if out_k is not None:
+        _out(out_k, "out_k", cache.dtype, shape, cache)
+    if out_v is not None:
+        _out(out_v, "out_v", cache.dtype, shape, cache)
+
+    def call(raw):
+        ko = torch.empty(shape, dtype=cache.dtype, device=cache.device) if out_k is None else out_k
+        vo = torch.empty(shape, dtype=cache.dtype, device=cache.device) if out_v is None else out_v
         st = cache_lib().spec_cache_read(ctypes.byref(cache.struct(page_table, lens)), B, n,
-                                         None if first is None else first.data_ptr(), out_k.data_ptr(),
-                                         out_v.data_ptr(), raw)
-    if st != 0:
-        _fail(st, "spec_cache_read")
-    return out_k, out_v
+                                         None if first is None else first.data_ptr(), ko.data_ptr(), vo.data_ptr(), raw)
+        if st != 0:
+            _fail(st, "spec_cache_read")
+        return ko, vo
+
+    return _on(cache, stream, call)

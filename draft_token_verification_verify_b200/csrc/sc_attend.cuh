@@ -39,6 +39,7 @@ struct AttendParams {
     long long q_stride, kv_stride;  // elements between tokens
     int B, n, q_heads, group;
     int rows, row_blocks;  // n * group, in blocks of SC_ROWS (or the tensor-memory kernel's width)
+    int whole;  // a CTA takes one whole segment: nothing is cut, and there is no K_join (and no status)
     float scale;
     void* out;
     float* out_lse;
@@ -80,6 +81,15 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) 
     __shared__ long long scan[NT / 32];
     __shared__ long long found[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (P.whole) {  // (not a range of units: the segment's number)
+        const int segs = P.c.kv_heads * P.row_blocks;
+        Range r;
+        r.b = static_cast<int>(blockIdx.x) / segs;
+        r.g0 = blockIdx.x - r.b * segs;
+        r.g1 = r.g0 + 1;
+        r.total = r.chunk = r.before = 0;
+        return r;
+    }
     const int per = (P.B + NT - 1) / NT;
     const long long segs = static_cast<long long>(P.c.kv_heads) * P.row_blocks;
     long long mine = 0;
@@ -146,6 +156,12 @@ struct Walk {
     __device__ __forceinline__ void begin(const AttendParams& P, const Range& r) {
         b = __shfl_sync(0xffffffffu, r.b, 0);
         sequence(P);
+        if (P.whole) {
+            hr = __shfl_sync(0xffffffffu, static_cast<int>(r.g0), 0);
+            u0 = left = 0;
+            u1 = units;
+            return;
+        }
         const long long in = r.g0 - r.before;
         hr = __shfl_sync(0xffffffffu, static_cast<int>(static_cast<double>(in) / units), 0);  // exact below 2^53
         u0 = __shfl_sync(0xffffffffu, static_cast<int>(in - static_cast<long long>(hr) * units), 0);
@@ -226,7 +242,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     pdl_launch_dependents();
     const Range R = sc_range<SC_NT, SC_BLOCK>(P, SC_MIN_TILES);
     bool error = false;
-    if (tid == 0) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !P.whole) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (R.g0 >= R.g1) return;
     if (mb == 0 && lane == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -795,7 +811,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         for (; used < issued; ++used)
             if (!sc_wait(&full[used % STAGES], (used / STAGES) & 1, P.timeout_ns)) error = true;
     }
-    if (error && lane == 0) P.desc[blockIdx.x].w = 1;
+    if (error && lane == 0 && !P.whole) P.desc[blockIdx.x].w = 1;
 }
 
 // K_join: block (i, j) adds the parts of the segment that is cut in CTA i and

@@ -9,11 +9,11 @@ namespace sv {
 namespace {
 template <int DT, int D, int MB>
 AttendKernel warps() {
-    return {sc_attend_kernel<DT, D, MB>, SC_NT, AttendSmem<D, MB>::BYTES, AttendSmem<D, MB>::ROWS, 2};
+    return {sc_attend_kernel<DT, D, MB>, SC_NT, AttendSmem<D, MB>::BYTES, AttendSmem<D, MB>::ROWS, 2, SC_BLOCK};
 }
 template <int DT, int D, int N, bool ALT>
 AttendKernel tensor_memory() {
-    return {sc_attend_tc_kernel<DT, D, N, ALT>, TC_NT, TcShape<DT, D, N, ALT>::BYTES, N, 1};
+    return {sc_attend_tc_kernel<DT, D, N, ALT>, TC_NT, TcShape<DT, D, N, ALT>::BYTES, N, 1, TC_TILE};
 }
 }  // namespace
 

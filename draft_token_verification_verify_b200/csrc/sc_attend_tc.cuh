@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
 
     pdl_launch_dependents();
     const Range R = sc_range<TC_NT, TC_TILE>(P, TC_MIN_TILES);
-    if (tid == 0) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !P.whole) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (R.g0 >= R.g1) return;
     if (tid == 0) {
 #pragma unroll 1
@@ -1068,7 +1068,7 @@ __global__ void __launch_bounds__(TC_NT, 1) sc_attend_tc_kernel(const __grid_con
         __syncwarp();
         tc_after();
         tc_dealloc(tmem, 512);
-        if (lane == 0 && *err_s) P.desc[blockIdx.x].w = 1;
+        if (lane == 0 && *err_s && !P.whole) P.desc[blockIdx.x].w = 1;
     }
 }
 

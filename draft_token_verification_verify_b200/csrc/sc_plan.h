@@ -10,6 +10,7 @@ struct AttendKernel {
     int threads, smem;  // of a CTA
     int block_rows;     // rows a CTA takes at once
     int per_sm;         // CTAs an SM holds
+    int tile;           // tokens of a tile
 };
 
 constexpr int SC_MOST_ROWS = 80;  // of a block

@@ -1,11 +1,12 @@
 // Writing the 4-bit cache and reading it back.
 //
 // K_append quantises the kept rows behind each sequence's length; K_read
-// expands a range of every sequence.  In both a group of D / 4 lanes (a warp
-// at D = 128, half a warp at D = 64) takes one (sequence, block of up to 64
-// tokens, head) and each lane 4 dims, so that the word of 8 tokens of a value
-// row (values are stored dim by dim) is built, or taken apart, within one lane.
-// Both are bound by the bytes they move; nothing is read twice.
+// expands a range of every sequence.  In both a group of D / 4 lanes (a warp at
+// D = 128, half a warp at D = 64) takes one (sequence, 8 tokens of a block,
+// head) and each lane 4 dims, so that the word of 8 tokens of a value row
+// (values are stored dim by dim) is built, or taken apart, within one lane.
+// Heads are the fastest index of the groups: neighbours read, or write, whole
+// token rows.  Both are bound by the bytes they move; nothing is read twice.
 #pragma once
 
 #include "sc_common.cuh"
@@ -23,7 +24,7 @@ struct AppendParams {
     const int32_t* nodes;       // or null
     int nodes_stride;
     int32_t* out_lens;  // null when a later kernel advances the lengths in place
-    int nblk;           // blocks a sequence's new rows can touch
+    int ngrp;           // groups of 8 positions a sequence's new rows can touch
 };
 
 struct ReadParams {
@@ -31,7 +32,7 @@ struct ReadParams {
     void* out_k;
     void* out_v;
     int B, n;
-    int nblk;
+    int ngrp;
 };
 
 // min of bf16 / fp16 pairs, NaN if either is.
@@ -95,19 +96,35 @@ __device__ __forceinline__ void sc_fold(uint32_t (&x)[16], int l, unsigned mask)
     }
 }
 
-// The code of an element as a float: (x - zero) / scale rounded to the nearest
+// The codes of 4 elements as floats: (x - zero) / scale rounded to the nearest
 // whole number, ties to even, as the exact fp32 quotient decides.  The product
-// with the reciprocal is within 1e-5 of that quotient; where it comes that
-// close to a half, or the reciprocal is of no use (NaN), the quotient is formed.
-__device__ __forceinline__ float sc_code(float x, float zero, float scale, float inv) {
-    const float d = __fsub_rn(x, zero);
-    const float q = d * inv;
-    float c = (fminf(q, 15.f) + 12582912.f) - 12582912.f;
-    if (!(fabsf(q - c) < 0.49998f)) {
-        c = scale > 0.f ? fminf(rintf(__fdiv_rn(d, scale)), 15.f) : 0.f;
-        if (!(c >= 0.f)) c = 0.f;
+// with the reciprocal is within 1e-5 of that quotient (which stays below 15.1
+// while the scale is a normal number); where it comes that close to a half, or
+// the reciprocal is of no use (NaN), the quotients are formed.
+__device__ __forceinline__ float sc_code(float d, float scale) {
+    const float c = scale > 0.f ? fminf(rintf(__fdiv_rn(d, scale)), 15.f) : 0.f;
+    return c >= 0.f ? c : 0.f;
+}
+__device__ __forceinline__ void sc_codes4(uint64_t x01, uint64_t x23, float zero, float scale, float inv,
+                                          uint64_t& c01, uint64_t& c23) {
+    const uint64_t nz = f2_pack(-zero, -zero), i2 = f2_pack(inv, inv);
+    const uint64_t up = f2_pack(12582912.f, 12582912.f), down = f2_pack(-12582912.f, -12582912.f);
+    const uint64_t d01 = f2_add(x01, nz), d23 = f2_add(x23, nz);
+    const uint64_t q01 = f2_mul(d01, i2), q23 = f2_mul(d23, i2);
+    c01 = f2_add(f2_add(q01, up), down);
+    c23 = f2_add(f2_add(q23, up), down);
+    float a, b, c, d, e0, e1, e2, e3;
+    f2_unpack(c01, a, b);
+    f2_unpack(c23, c, d);
+    f2_unpack(q01, e0, e1);
+    f2_unpack(q23, e2, e3);
+    const float off = fmaxf(fmaxf(fabsf(e0 - a), fabsf(e1 - b)), fmaxf(fabsf(e2 - c), fabsf(e3 - d)));
+    if (off >= 0.49998f || inv != inv) {
+        f2_unpack(d01, a, b);
+        f2_unpack(d23, c, d);
+        c01 = f2_pack(sc_code(a, scale), sc_code(b, scale));
+        c23 = f2_pack(sc_code(c, scale), sc_code(d, scale));
     }
-    return c;
 }
 
 // Low 16 bits: a whole number below 2^16 held in a float.
@@ -122,8 +139,8 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
     const long long item = (static_cast<long long>(blockIdx.x) * SC_STORE_NT + threadIdx.x) / LPI;
     const int h = static_cast<int>(item % c.kv_heads);
     const long long bj = item / c.kv_heads;
-    const int j = static_cast<int>(bj % P.nblk);
-    const long long bl = bj / P.nblk;
+    const int j = static_cast<int>(bj % P.ngrp);
+    const long long bl = bj / P.ngrp;
     if (bl >= P.B) return;
     const int b = static_cast<int>(bl);
     if (P.out_lens && h == 0 && j == 0) {
@@ -133,101 +150,106 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
     int len, count;
     if (!sc_kept(c, P, b, &len, &count) || count == 0) return;
     const int T = c.block;
-    const int blk = (len >> c.log2_block) + j;  // block of the sequence
-    const int t0 = blk << c.log2_block;
+    const int p0 = ((len >> 3) + j) << 3;  // first position of the group
+    if (p0 >= len + count) return;
+    const int t0 = p0 & ~(T - 1);          // and of its block
     const int from = len > t0 ? len - t0 : 0;                     // tokens of the block written:
     const int to = len + count - t0 < T ? len + count - t0 : T;  // [from, to)
-    if (from >= to) return;
     const int id = c.table[static_cast<size_t>(b) * c.max_pages + (t0 >> c.log2_page)];
     if (id < 0 || id >= c.num_pages) return;
     unsigned char* blkp = sc_block_ptr<D>(c, id, h, (t0 & (c.page_size - 1)) >> c.log2_block);
     unsigned char* vblk = blkp + sc_half_bytes<D>(T);
 
-    for (int g = from >> 3; g * 8 < to; ++g) {
-        // 8 tokens: 4 dims of each, keys and values
-        uint2 raw[16];
-        bool have[8];
+    const int g = (p0 - t0) >> 3;
+    // 8 tokens: 4 dims of each, keys and values
+    uint2 raw[16];
+    uint32_t have = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int t = g * 8 + i;
-            have[i] = false;
-            raw[i] = raw[8 + i] = make_uint2(0u, 0u);
-            if (t >= from && t < to) {
-                const int node = sc_node(P, b, t0 + t - len);
-                if (node >= 0 && node < P.n) {
-                    have[i] = true;
-                    const size_t o = (static_cast<size_t>(b) * P.n + node) * static_cast<size_t>(P.stride) +
-                                     static_cast<size_t>(h) * D + 4 * l;
-                    raw[i] = *reinterpret_cast<const uint2*>(static_cast<const typename Ty::T*>(P.k) + o);
-                    raw[8 + i] = *reinterpret_cast<const uint2*>(static_cast<const typename Ty::T*>(P.v) + o);
-                }
+    for (int i = 0; i < 8; ++i) {
+        const int t = g * 8 + i;
+        raw[i] = raw[8 + i] = make_uint2(0u, 0u);
+        if (t >= from && t < to) {
+            const int node = sc_node(P, b, t0 + t - len);
+            if (node >= 0 && node < P.n) {
+                have |= 1u << i;
+                const size_t o = (static_cast<size_t>(b) * P.n + node) * static_cast<size_t>(P.stride) +
+                                 static_cast<size_t>(h) * D + 4 * l;
+                raw[i] = *reinterpret_cast<const uint2*>(static_cast<const typename Ty::T*>(P.k) + o);
+                raw[8 + i] = *reinterpret_cast<const uint2*>(static_cast<const typename Ty::T*>(P.v) + o);
             }
         }
-        // each row's {min, -max}: within the lane, then a reduce-scatter of the
-        // 16 rows over the lanes (15 exchanges of one register, and one more at
-        // 32 lanes, in place of 5 steps for each row and side)
-        uint32_t x[16];
+    }
+    // each row's {min, -max}: within the lane, then a reduce-scatter of the
+    // 16 rows over the lanes (15 exchanges of one register, and one more at
+    // 32 lanes, in place of 5 steps for each row and side)
+    uint32_t x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t lo = sc_min2<DT>(raw[i].x, raw[i].y);
-            const uint32_t hi = sc_min2<DT>(raw[i].x ^ 0x80008000u, raw[i].y ^ 0x80008000u);
-            x[i] = sc_min2<DT>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
-        }
-        sc_fold<DT, 16, 1>(x, l, mask);
-        sc_fold<DT, 8, 2>(x, l, mask);
-        sc_fold<DT, 4, 4>(x, l, mask);
-        sc_fold<DT, 2, 8>(x, l, mask);
-        if (LPI == 32) x[0] = sc_min2<DT>(x[0], __shfl_xor_sync(mask, x[0], 16));
-        // lane l holds row 8 b0 + 4 b1 + 2 b2 + b3 (b the bits of l): its (scale, zero)
-        uint32_t par;
-        {
-            const float mn = Ty::lo(x[0]), mx = -Ty::hi(x[0]);
-            const float sc = Ty::round(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
-            const bool fine = fabsf(mn) < __builtin_huge_valf() && fabsf(mx) < __builtin_huge_valf() &&
-                              fabsf(sc) < __builtin_huge_valf();
-            par = fine ? Ty::pack(sc, mn) : 0x00007fffu;  // a NaN in either type
-        }
-        uint32_t word[4][2];  // 8 tokens of each of the lane's value dims: halves
-        float vacc[4][2];
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t lo = sc_min2<DT>(raw[i].x, raw[i].y);
+        const uint32_t hi = sc_min2<DT>(raw[i].x ^ 0x80008000u, raw[i].y ^ 0x80008000u);
+        x[i] = sc_min2<DT>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+    }
+    sc_fold<DT, 16, 1>(x, l, mask);
+    sc_fold<DT, 8, 2>(x, l, mask);
+    sc_fold<DT, 4, 4>(x, l, mask);
+    sc_fold<DT, 2, 8>(x, l, mask);
+    if (LPI == 32) x[0] = sc_min2<DT>(x[0], __shfl_xor_sync(mask, x[0], 16));
+    // lane l holds row 8 b0 + 4 b1 + 2 b2 + b3 (b the bits of l): its (scale, zero), and what a
+    // difference from zero is multiplied by (NaN: it is divided, see sc_codes4)
+    uint32_t par;
+    float inv;
+    {
+        const float mn = Ty::lo(x[0]), mx = -Ty::hi(x[0]);
+        const float sc = Ty::round(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
+        const bool fine = fabsf(mn) < __builtin_huge_valf() && fabsf(mx) < __builtin_huge_valf() &&
+                          fabsf(sc) < __builtin_huge_valf();
+        par = fine ? Ty::pack(sc, mn) : 0x00007fffu;  // a NaN in either type
+        inv = fine && sc >= (DT == 0 ? 1e-30f : 6.2e-5f) ? __fdividef(1.f, sc) : __int_as_float(0x7fffffff);
+    }
+    uint64_t vacc[2][2];  // dims {0, 1} and {2, 3} of the lane: the even and the odd tokens' codes
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int src = ((i >> 3) & 1) | ((i >> 1) & 2) | ((i << 1) & 4) | ((i << 3) & 8);
-            const uint32_t p = __shfl_sync(mask, par, src, LPI);
-            const float sc = Ty::lo(p), zero = Ty::hi(p);
-            const float inv = sc > 1e-30f ? __fdividef(1.f, sc) : (sc == 0.f ? 0.f : __int_as_float(0x7fffffff));
-            const float c0 = sc_code(Ty::lo(raw[i].x), zero, sc, inv), c1 = sc_code(Ty::hi(raw[i].x), zero, sc, inv);
-            const float c2 = sc_code(Ty::lo(raw[i].y), zero, sc, inv), c3 = sc_code(Ty::hi(raw[i].y), zero, sc, inv);
-            const int t = g * 8 + (i & 7);
-            if (i < 8) {
-                // a key row's word w: dims 8w.. from lanes 2w (low byte of each half) and 2w+1
-                uint32_t w = __byte_perm(sc_bits(fmaf(16.f, c2, c0)), sc_bits(fmaf(16.f, c3, c1)),
-                                         (l & 1) ? 0x4707 : 0x7470) &
-                             ((l & 1) ? 0xFF00FF00u : 0x00FF00FFu);
-                w |= __shfl_xor_sync(mask, w, 1);
-                if (have[i & 7]) {
-                    if ((l & 1) == 0) *reinterpret_cast<uint32_t*>(blkp + t * (D / 2) + (l >> 1) * 4) = w;
-                    if (l == 1) *reinterpret_cast<uint32_t*>(blkp + T * (D / 2) + t * 4) = p;
-                }
-            } else {
-                const float cc[4] = {c0, c1, c2, c3};
-                const int e = i & 1, m = (i & 7) >> 1;  // token 2m + e: bits 16e + 4m
-                const float f = m == 0 ? 1.f : m == 1 ? 16.f : m == 2 ? 256.f : 4096.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) vacc[q][e] = m == 0 ? cc[q] : fmaf(f, cc[q], vacc[q][e]);
-                if (l == 0 && have[i & 7]) *reinterpret_cast<uint32_t*>(vblk + T * (D / 2) + t * 4) = p;
+    for (int i = 0; i < 16; ++i) {
+        const int src = ((i >> 3) & 1) | ((i >> 1) & 2) | ((i << 1) & 4) | ((i << 3) & 8);
+        const uint32_t p = __shfl_sync(mask, par, src, LPI);
+        const float iv = __shfl_sync(mask, inv, src, LPI);
+        uint64_t c01, c23;
+        sc_codes4(f2_pack(Ty::lo(raw[i].x), Ty::hi(raw[i].x)), f2_pack(Ty::lo(raw[i].y), Ty::hi(raw[i].y)), Ty::hi(p),
+                  Ty::lo(p), iv, c01, c23);
+        const int t = g * 8 + (i & 7);
+        const bool mine = (have >> (i & 7)) & 1u;
+        if (i < 8) {
+            // a key row's word w: dims 8w.. from lanes 2w (low byte of each half) and 2w+1
+            float lo, hi;
+            f2_unpack(f2_fma(f2_pack(16.f, 16.f), c23, c01), lo, hi);
+            uint32_t w = __byte_perm(sc_bits(lo), sc_bits(hi), (l & 1) ? 0x4707 : 0x7470) &
+                         ((l & 1) ? 0xFF00FF00u : 0x00FF00FFu);
+            w |= __shfl_xor_sync(mask, w, 1);
+            if (mine) {
+                if ((l & 1) == 0) *reinterpret_cast<uint32_t*>(blkp + t * (D / 2) + (l >> 1) * 4) = w;
+                if (l == 1) *reinterpret_cast<uint32_t*>(blkp + T * (D / 2) + t * 4) = p;
             }
+        } else {
+            const int e = i & 1, m = (i & 7) >> 1;  // token 2m + e: bits 16e + 4m
+            const float f = m == 1 ? 16.f : m == 2 ? 256.f : 4096.f;
+            vacc[0][e] = m == 0 ? c01 : f2_fma(f2_pack(f, f), c01, vacc[0][e]);
+            vacc[1][e] = m == 0 ? c23 : f2_fma(f2_pack(f, f), c23, vacc[1][e]);
+            if (l == 0 && mine) *reinterpret_cast<uint32_t*>(vblk + T * (D / 2) + t * 4) = p;
         }
-        // tokens of the group that are not written keep their codes
-        uint32_t keep = 0;
+    }
+    // tokens of the group that are not written keep their codes
+    uint32_t keep = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!have[i]) keep |= 0xFu << (16 * (i & 1) + 4 * (i >> 1));
+    for (int i = 0; i < 8; ++i)
+        if (!((have >> i) & 1u)) keep |= 0xFu << (16 * (i & 1) + 4 * (i >> 1));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            word[q][0] = sc_bits(vacc[q][0]);
-            word[q][1] = sc_bits(vacc[q][1]);
-            uint32_t w = __byte_perm(word[q][0], word[q][1], 0x5410);
-            uint32_t* dst = reinterpret_cast<uint32_t*>(vblk + (4 * l + q) * (T / 2) + g * 4);
+    for (int q = 0; q < 2; ++q) {
+        float e0, e1, o0, o1;
+        f2_unpack(vacc[q][0], e0, e1);
+        f2_unpack(vacc[q][1], o0, o1);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w = __byte_perm(sc_bits(k ? e1 : e0), sc_bits(k ? o1 : o0), 0x5410);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(vblk + (4 * l + 2 * q + k) * (T / 2) + g * 4);
             if (keep) w = (w & ~keep) | (*dst & keep);
             *dst = w;
         }
@@ -257,17 +279,18 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_read_kernel(CacheView c, ReadP
     const long long item = (static_cast<long long>(blockIdx.x) * SC_STORE_NT + threadIdx.x) / LPI;
     const int h = static_cast<int>(item % c.kv_heads);
     const long long bj = item / c.kv_heads;
-    const int j = static_cast<int>(bj % P.nblk);
-    const long long bl = bj / P.nblk;
+    const int j = static_cast<int>(bj % P.ngrp);
+    const long long bl = bj / P.ngrp;
     if (bl >= P.B) return;
     const int b = static_cast<int>(bl);
     const int len = c.lens[b];
     const long long first = P.first ? P.first[b] : 0;
     const int T = c.block;
-    const long long t0 = ((first >> c.log2_block) + j) << c.log2_block;  // may be negative
+    const long long p0 = ((first >> 3) + j) * 8;  // first position of the group, may be negative
+    if (p0 >= first + P.n) return;
+    const long long t0 = p0 & ~static_cast<long long>(T - 1);  // and of its block
     const int from = static_cast<int>(first > t0 ? first - t0 : 0);
     const int to = static_cast<int>(first + P.n - t0 < T ? first + P.n - t0 : T);
-    if (from >= to) return;
     const unsigned char* blkp = nullptr;
     bool bad = false;
     if (t0 >= 0 && t0 < len) {
@@ -282,7 +305,8 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_read_kernel(CacheView c, ReadP
     const unsigned char* vblk = blkp ? blkp + sc_half_bytes<D>(T) : nullptr;
     typename Ty::T* ok = static_cast<typename Ty::T*>(P.out_k);
     typename Ty::T* ov = static_cast<typename Ty::T*>(P.out_v);
-    for (int g = from >> 3; g * 8 < to; ++g) {
+    const int g = static_cast<int>(p0 - t0) >> 3;
+    {
         uint32_t vw[4] = {0u, 0u, 0u, 0u}, kw[8];
         uint32_t kp[8], vp[8];
 #pragma unroll

@@ -17,6 +17,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
 constexpr int kMaxPage = 1024;
+constexpr long long kWholeTokens = 1024;  // contexts up to this are not cut
 
 struct DeviceInfo {
     bool ok = false;
@@ -112,7 +113,7 @@ bool make_plan(const DeviceInfo& d, int B, int n, int q_heads, int kv_heads, int
     p->off_ml = round_up(parts * D * sizeof(float), 256);
     p->off_desc = p->off_ml + round_up(parts * sizeof(float2), 256);
     p->bytes = p->off_desc + round_up(static_cast<size_t>(p->grid) * sizeof(int4), 256);
-    return static_cast<long long>(B) * kv_heads * p->row_blocks <= (1LL << 31);
+    return static_cast<long long>(B) * kv_heads * p->row_blocks < (1LL << 31);
 }
 
 bool attend_sizes_ok(int B, int n, int q_heads, int kv_heads) {
@@ -204,6 +205,13 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     P.rows = n * P.group;
     P.row_blocks = plan.row_blocks;
     P.scale = scale;
+    // Short contexts (by the page table's width, the lengths being on the device): a CTA takes a whole
+    // segment, and one launch does.  That costs less than the join up to
+    // kWholeTokens a segment.
+    const long long tiles = ceil_div(static_cast<long long>(cache->max_pages) * cache->page_size, plan.k.tile) +
+                            (k_new ? ceil_div(n, plan.k.tile) : 0);
+    P.whole = tiles * plan.k.tile <= kWholeTokens && !out_status;
+    if (P.whole) plan.grid = static_cast<int>(static_cast<long long>(B) * cache->kv_heads * plan.row_blocks);
     P.out = out;
     P.out_lse = out_lse;
     auto* ws = static_cast<unsigned char*>(workspace);
@@ -231,6 +239,7 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
         r = launched(cudaEventRecord(static_cast<cudaEvent_t>(opts->event_stop), st));
         if (r != SV_OK) return r;
     }
+    if (P.whole) return SV_OK;
     cudaLaunchAttribute a[1];
     a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     a[0].val.programmaticStreamSerializationAllowed = 1;
@@ -269,8 +278,8 @@ sv_status_t spec_cache_append(const sv_cache_t* cache, const void* k, const void
     P.nodes = nodes;
     P.nodes_stride = nodes_stride;
     P.out_lens = in_place ? nullptr : out_lens;
-    P.nblk = static_cast<int>((static_cast<long long>(n) + c.block - 2) / c.block + 1);
-    const long long items = static_cast<long long>(B) * P.nblk * c.kv_heads;
+    P.ngrp = static_cast<int>((static_cast<long long>(n) + 6) / 8 + 1);
+    const long long items = static_cast<long long>(B) * P.ngrp * c.kv_heads;
     const long long blocks = ceil_div(items, sv::SC_STORE_NT / (D / 4));
     if (blocks > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -311,8 +320,8 @@ sv_status_t spec_cache_read(const sv_cache_t* cache, int B, int n, const int32_t
     P.out_v = out_v;
     P.B = B;
     P.n = n;
-    P.nblk = static_cast<int>((static_cast<long long>(n) + c.block - 2) / c.block + 1);
-    const long long items = static_cast<long long>(B) * P.nblk * c.kv_heads;
+    P.ngrp = static_cast<int>((static_cast<long long>(n) + 6) / 8 + 1);
+    const long long items = static_cast<long long>(B) * P.ngrp * c.kv_heads;
     const long long blocks = ceil_div(items, sv::SC_STORE_NT / (D / 4));
     if (blocks > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
     void (*fn)(sv::CacheView, sv::ReadParams) = D == 64 ? (dt ? sv::sc_read_kernel<1, 64> : sv::sc_read_kernel<0, 64>)

@@ -145,8 +145,8 @@ def test_token_strides():
 
     c = sv.KvCache.empty(4, 2, 64, 128, device="cpu")
     rows = torch.zeros((2, 3, 8, 128), dtype=torch.bfloat16)
-    assert _tokens(rows, "x", c) == 8 * 128 and _tokens(rows[:, :, 4:6], "x", c, 2) == 8 * 128
-    assert _tokens(rows[:, :1], "x", c) == 3 * 8 * 128 and _tokens(rows[:1, :1, :2], "x", c) == 2 * 128
+    assert _tokens(rows, "x", c)[1] == 8 * 128 and _tokens(rows[:, :, 4:6], "x", c, 2)[1] == 8 * 128
+    assert _tokens(rows[:, :1], "x", c)[1] == 3 * 8 * 128 and _tokens(rows[:1, :1, :2], "x", c)[1] == 2 * 128
     for bad, err in ((rows.float(), TypeError), (rows[..., :64], ValueError), (rows[:, :2], ValueError),
                      (rows[:, :, ::2], ValueError), (rows[:, :, :, 1:], ValueError), (rows.transpose(0, 1), ValueError),
                      (rows[:0], ValueError), (rows[0], ValueError), (None, TypeError)):
