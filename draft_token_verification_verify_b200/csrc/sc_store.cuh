@@ -100,10 +100,32 @@ __device__ __forceinline__ void sc_fold(uint32_t (&x)[16], int l, unsigned mask)
 // whole number, ties to even, as the exact fp32 quotient decides.  The product
 // with the reciprocal is within 1e-5 of that quotient (which stays below 15.1
 // while the scale is a normal number); where it comes that close to a half, or
-// the reciprocal is of no use (NaN), the quotients are formed.
-__device__ __forceinline__ float sc_code(float d, float scale) {
-    const float c = scale > 0.f ? fminf(rintf(__fdiv_rn(d, scale)), 15.f) : 0.f;
-    return c >= 0.f ? c : 0.f;
+// the reciprocal is of no use (NaN), sc_near decides.
+__device__ __noinline__ void sc_near(uint64_t d01, uint64_t d23, float scale, float inv, uint64_t& c01, uint64_t& c23) {
+    float d[4], c[4];
+    f2_unpack(d01, d[0], d[1]);
+    f2_unpack(d23, d[2], d[3]);
+    f2_unpack(c01, c[0], c[1]);
+    f2_unpack(c23, c[2], c[3]);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const float e = d[i] * inv - c[i];
+        if (fabsf(e) < 0.49998f) continue;
+        // the half between two codes, and on which side of it the quotient lies (the sign of the fused
+        // difference is exact); too close to tell by that, or no reciprocal: divide
+        const float h = c[i] + (e > 0.f ? 0.5f : -0.5f);
+        const float r = fmaf(-h, scale, d[i]);
+        float x;
+        if (fabsf(r) > 1e-6f * d[i]) {
+            x = r > 0.f ? h + 0.5f : h - 0.5f;
+        } else {
+            x = scale > 0.f ? fminf(rintf(__fdiv_rn(d[i], scale)), 15.f) : 0.f;
+            if (!(x >= 0.f)) x = 0.f;
+        }
+        c[i] = x;
+    }
+    c01 = f2_pack(c[0], c[1]);
+    c23 = f2_pack(c[2], c[3]);
 }
 __device__ __forceinline__ void sc_codes4(uint64_t x01, uint64_t x23, float zero, float scale, float inv,
                                           uint64_t& c01, uint64_t& c23) {
@@ -119,12 +141,7 @@ __device__ __forceinline__ void sc_codes4(uint64_t x01, uint64_t x23, float zero
     f2_unpack(q01, e0, e1);
     f2_unpack(q23, e2, e3);
     const float off = fmaxf(fmaxf(fabsf(e0 - a), fabsf(e1 - b)), fmaxf(fabsf(e2 - c), fabsf(e3 - d)));
-    if (off >= 0.49998f || inv != inv) {
-        f2_unpack(d01, a, b);
-        f2_unpack(d23, c, d);
-        c01 = f2_pack(sc_code(a, scale), sc_code(b, scale));
-        c23 = f2_pack(sc_code(c, scale), sc_code(d, scale));
-    }
+    if (off >= 0.49998f || inv != inv) sc_near(d01, d23, scale, inv, c01, c23);
 }
 
 // Low 16 bits: a whole number below 2^16 held in a float.
@@ -163,19 +180,39 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
     const int g = (p0 - t0) >> 3;
     // 8 tokens: 4 dims of each, keys and values
     uint2 raw[16];
-    uint32_t have = 0;
+    uint32_t have = 0xffu;
+    {
+        const typename Ty::T* kp = static_cast<const typename Ty::T*>(P.k) + static_cast<size_t>(h) * D + 4 * l;
+        const typename Ty::T* vp = static_cast<const typename Ty::T*>(P.v) + static_cast<size_t>(h) * D + 4 * l;
+        const size_t row = static_cast<size_t>(b) * P.n;
+        if (!P.nodes && from <= g * 8 && g * 8 + 8 <= to) {  // a whole group of rows side by side
+            const size_t o = (row + (p0 - len)) * static_cast<size_t>(P.stride);
+            kp += o;
+            vp += o;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int t = g * 8 + i;
-        raw[i] = raw[8 + i] = make_uint2(0u, 0u);
-        if (t >= from && t < to) {
-            const int node = sc_node(P, b, t0 + t - len);
-            if (node >= 0 && node < P.n) {
-                have |= 1u << i;
-                const size_t o = (static_cast<size_t>(b) * P.n + node) * static_cast<size_t>(P.stride) +
-                                 static_cast<size_t>(h) * D + 4 * l;
-                raw[i] = *reinterpret_cast<const uint2*>(static_cast<const typename Ty::T*>(P.k) + o);
-                raw[8 + i] = *reinterpret_cast<const uint2*>(static_cast<const typename Ty::T*>(P.v) + o);
+            for (int i = 0; i < 8; ++i) {
+                raw[i] = *reinterpret_cast<const uint2*>(kp);
+                raw[8 + i] = *reinterpret_cast<const uint2*>(vp);
+                kp += P.stride;
+                vp += P.stride;
+            }
+        } else {
+            have = 0;
+            int node[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = g * 8 + i;
+                node[i] = t >= from && t < to ? sc_node(P, b, t0 + t - len) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                raw[i] = raw[8 + i] = make_uint2(0u, 0u);
+                if (node[i] >= 0 && node[i] < P.n) {
+                    have |= 1u << i;
+                    const size_t o = (row + node[i]) * static_cast<size_t>(P.stride);
+                    raw[i] = *reinterpret_cast<const uint2*>(kp + o);
+                    raw[8 + i] = *reinterpret_cast<const uint2*>(vp + o);
+                }
             }
         }
     }
@@ -206,6 +243,12 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
         par = fine ? Ty::pack(sc, mn) : 0x00007fffu;  // a NaN in either type
         inv = fine && sc >= (DT == 0 ? 1e-30f : 6.2e-5f) ? __fdividef(1.f, sc) : __int_as_float(0x7fffffff);
     }
+    if (l < 16) {
+        const int i = 8 * (l & 1) + 4 * ((l >> 1) & 1) + 2 * ((l >> 2) & 1) + ((l >> 3) & 1);  // the lane's row
+        if ((have >> (i & 7)) & 1u)
+            *reinterpret_cast<uint32_t*>((i < 8 ? blkp : vblk) + T * (D / 2) + (g * 8 + (i & 7)) * 4) = par;
+    }
+    uint32_t before = 0;
     uint64_t vacc[2][2];  // dims {0, 1} and {2, 3} of the lane: the even and the odd tokens' codes
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -215,8 +258,6 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
         uint64_t c01, c23;
         sc_codes4(f2_pack(Ty::lo(raw[i].x), Ty::hi(raw[i].x)), f2_pack(Ty::lo(raw[i].y), Ty::hi(raw[i].y)), Ty::hi(p),
                   Ty::lo(p), iv, c01, c23);
-        const int t = g * 8 + (i & 7);
-        const bool mine = (have >> (i & 7)) & 1u;
         if (i < 8) {
             // a key row's word w: dims 8w.. from lanes 2w (low byte of each half) and 2w+1
             float lo, hi;
@@ -224,16 +265,17 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
             uint32_t w = __byte_perm(sc_bits(lo), sc_bits(hi), (l & 1) ? 0x4707 : 0x7470) &
                          ((l & 1) ? 0xFF00FF00u : 0x00FF00FFu);
             w |= __shfl_xor_sync(mask, w, 1);
-            if (mine) {
-                if ((l & 1) == 0) *reinterpret_cast<uint32_t*>(blkp + t * (D / 2) + (l >> 1) * 4) = w;
-                if (l == 1) *reinterpret_cast<uint32_t*>(blkp + T * (D / 2) + t * 4) = p;
+            if (i & 1) {  // the even lanes store the token before, the odd ones this
+                const int t = i - 1 + (l & 1);
+                if ((have >> t) & 1u)
+                    *reinterpret_cast<uint32_t*>(blkp + (g * 8 + t) * (D / 2) + (l >> 1) * 4) = (l & 1) ? w : before;
             }
+            before = w;
         } else {
             const int e = i & 1, m = (i & 7) >> 1;  // token 2m + e: bits 16e + 4m
             const float f = m == 1 ? 16.f : m == 2 ? 256.f : 4096.f;
             vacc[0][e] = m == 0 ? c01 : f2_fma(f2_pack(f, f), c01, vacc[0][e]);
             vacc[1][e] = m == 0 ? c23 : f2_fma(f2_pack(f, f), c23, vacc[1][e]);
-            if (l == 0 && mine) *reinterpret_cast<uint32_t*>(vblk + T * (D / 2) + t * 4) = p;
         }
     }
     // tokens of the group that are not written keep their codes
@@ -264,11 +306,6 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_advance_kernel(CacheView c, Ap
     const int l = threadIdx.x & 31;
     const int nl = sc_new_len<32>(c, P, b, l, 0xffffffffu);
     if (l == 0) out_lens[b] = nl;
-}
-
-// Four codes at bit 0 (lane even) or 8 (odd) of a key word as floats.
-__device__ __forceinline__ float sc_code_f(uint32_t w, int shift) {
-    return __uint_as_float(((w >> shift) & 15u) | 0x4B000000u) - 8388608.f;
 }
 
 template <int DT, int D>
@@ -303,59 +340,81 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_read_kernel(CacheView c, ReadP
         }
     }
     const unsigned char* vblk = blkp ? blkp + sc_half_bytes<D>(T) : nullptr;
+    const int g = static_cast<int>(p0 - t0) >> 3;
+    // the group's words and parameters; nothing where its block cannot be read
+    uint32_t kw[8], vw[4], kp[8], vp[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) kw[i] = kp[i] = vp[i] = 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) vw[q] = 0u;
+    if (blkp) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const uint4 a = *reinterpret_cast<const uint4*>(blkp + T * (D / 2) + (g * 8 + i) * 4);
+            const uint4 e = *reinterpret_cast<const uint4*>(vblk + T * (D / 2) + (g * 8 + i) * 4);
+            kp[i] = a.x, kp[i + 1] = a.y, kp[i + 2] = a.z, kp[i + 3] = a.w;
+            vp[i] = e.x, vp[i + 1] = e.y, vp[i + 2] = e.z, vp[i + 3] = e.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            kw[i] = *reinterpret_cast<const uint32_t*>(blkp + (g * 8 + i) * (D / 2) + (l >> 1) * 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            vw[q] = *reinterpret_cast<const uint32_t*>(vblk + (4 * l + q) * (T / 2) + g * 4);
+    }
+    // rows of the group that are read, and of them those that hold a token
+    uint32_t rows = 0, in = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int t = g * 8 + i;
+        const long long pos = t0 + t;
+        if (t >= from && t < to) rows |= 1u << i;
+        if (pos >= 0 && pos < len) in |= 1u << i;
+    }
     typename Ty::T* ok = static_cast<typename Ty::T*>(P.out_k);
     typename Ty::T* ov = static_cast<typename Ty::T*>(P.out_v);
-    const int g = static_cast<int>(p0 - t0) >> 3;
-    {
-        uint32_t vw[4] = {0u, 0u, 0u, 0u}, kw[8];
-        uint32_t kp[8], vp[8];
+    const size_t step = static_cast<size_t>(c.kv_heads) * D;
+    // (of the group's first row, which may lie before the range)
+    const long long o0 = ((static_cast<long long>(b) * P.n + (p0 - first)) * c.kv_heads + h) * D + 4 * l;
+    const uint64_t down = f2_pack(-8388608.f, -8388608.f);
+    const uint32_t sel = 0x7540u + (l & 1);  // a byte of the codes below 2^23's upper bytes
+    uint32_t vlo[4], vhi[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            kw[i] = kp[i] = vp[i] = 0u;
-            const int t = g * 8 + i;
-            if (blkp && t >= from && t < to) {
-                if (ok) {
-                    kw[i] = *reinterpret_cast<const uint32_t*>(blkp + t * (D / 2) + (l >> 1) * 4);
-                    kp[i] = *reinterpret_cast<const uint32_t*>(blkp + T * (D / 2) + t * 4);
-                }
-                if (ov) vp[i] = *reinterpret_cast<const uint32_t*>(vblk + T * (D / 2) + t * 4);
-            }
+    for (int q = 0; q < 4; ++q) {
+        vlo[q] = vw[q] & 0x0F0F0F0Fu;
+        vhi[q] = (vw[q] >> 4) & 0x0F0F0F0Fu;
+    }
+    auto value = [&](uint32_t a, uint32_t e, uint64_t s2, uint64_t z2) {  // two codes as floats above 2^23
+        float x, y;
+        f2_unpack(f2_fma(s2, f2_add(f2_pack(__uint_as_float(a), __uint_as_float(e)), down), z2), x, y);
+        return Ty::pack(x, y);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (!((rows >> i) & 1u)) continue;
+        const bool token = (in >> i) & 1u;
+        const size_t o = static_cast<size_t>(o0 + static_cast<long long>(i) * static_cast<long long>(step));
+        const uint32_t fill = token && bad ? 0x7fff7fffu : 0u;
+        if (ok) {
+            const float s = Ty::lo(kp[i]), z = Ty::hi(kp[i]);
+            const uint64_t s2 = f2_pack(s, s), z2 = f2_pack(z, z);
+            const uint32_t lo = kw[i] & 0x0F0F0F0Fu, hi = (kw[i] >> 4) & 0x0F0F0F0Fu;
+            uint2 y = make_uint2(value(__byte_perm(lo, 0x4B000000u, sel), __byte_perm(lo, 0x4B000000u, sel + 2), s2, z2),
+                                 value(__byte_perm(hi, 0x4B000000u, sel), __byte_perm(hi, 0x4B000000u, sel + 2), s2, z2));
+            if (!token || bad) y = make_uint2(fill, fill);
+            *reinterpret_cast<uint2*>(ok + o) = y;
         }
-        if (blkp && ov) {
+        if (ov) {
+            const float s = Ty::lo(vp[i]), z = Ty::hi(vp[i]);
+            const uint64_t s2 = f2_pack(s, s), z2 = f2_pack(z, z);
+            // token i: nibble (i / 2) of the half i % 2, so byte i / 4 + 2 (i % 2), its upper half for i / 2 odd
+            const uint32_t vs = 0x7540u + (i >> 2) + 2 * (i & 1);
+            uint32_t x[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                vw[q] = *reinterpret_cast<const uint32_t*>(vblk + (4 * l + q) * (T / 2) + g * 4);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int t = g * 8 + i;
-            if (t < from || t >= to) continue;
-            const long long pos = t0 + t;
-            const size_t o = ((static_cast<size_t>(b) * P.n + static_cast<size_t>(pos - first)) * c.kv_heads + h) *
-                                 static_cast<size_t>(D) + 4 * l;
-            const bool in = pos >= 0 && pos < len;
-            if (ok) {
-                uint2 w = make_uint2(0u, 0u);
-                if (in && bad) w = make_uint2(0x7fff7fffu, 0x7fff7fffu);
-                if (in && !bad) {
-                    const float s = Ty::lo(kp[i]), z = Ty::hi(kp[i]);
-                    const uint32_t x = kw[i] >> (8 * (l & 1));
-                    w.x = Ty::pack(fmaf(s, sc_code_f(x, 0), z), fmaf(s, sc_code_f(x, 16), z));
-                    w.y = Ty::pack(fmaf(s, sc_code_f(x, 4), z), fmaf(s, sc_code_f(x, 20), z));
-                }
-                *reinterpret_cast<uint2*>(ok + o) = w;
-            }
-            if (ov) {
-                uint2 w = make_uint2(0u, 0u);
-                if (in && bad) w = make_uint2(0x7fff7fffu, 0x7fff7fffu);
-                if (in && !bad) {
-                    const float s = Ty::lo(vp[i]), z = Ty::hi(vp[i]);
-                    const int sh = 16 * (i & 1) + 4 * (i >> 1);
-                    w.x = Ty::pack(fmaf(s, sc_code_f(vw[0], sh), z), fmaf(s, sc_code_f(vw[1], sh), z));
-                    w.y = Ty::pack(fmaf(s, sc_code_f(vw[2], sh), z), fmaf(s, sc_code_f(vw[3], sh), z));
-                }
-                *reinterpret_cast<uint2*>(ov + o) = w;
-            }
+            for (int q = 0; q < 4; ++q) x[q] = __byte_perm(((i >> 1) & 1) ? vhi[q] : vlo[q], 0x4B000000u, vs);
+            uint2 y = make_uint2(value(x[0], x[1], s2, z2), value(x[2], x[3], s2, z2));
+            if (!token || bad) y = make_uint2(fill, fill);
+            *reinterpret_cast<uint2*>(ov + o) = y;
         }
     }
 }
