@@ -3,7 +3,6 @@ from __future__ import annotations
 
 import os
 import subprocess
-import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,10 +19,8 @@ def _csrc(*names):
 SOURCES = _csrc("spec_verify.cu")
 DEPS = SOURCES + _csrc("sv_common.cuh", "sv_rows.cuh", "sv_seq.cuh", "sv_resid.cuh", "sv_ptx.cuh", "sv_procs.cuh",
                        "sv_nucleus.cuh", "sv_tree.cuh", "sv_head.cuh") + [HEADER]
-CACHE_SOURCES = [(_csrc("spec_cache.cu")[0], [])] + [
-    (_csrc("sc_attend_inst.cu")[0], [f"-DSC_DT={dt}", f"-DSC_D={d}"]) for dt in (0, 1) for d in (64, 128)]
-CACHE_DEPS = _csrc("spec_cache.cu", "sc_attend_inst.cu", "sc_plan.h", "sc_common.cuh", "sc_attend.cuh",
-                   "sc_attend_tc.cuh", "sc_store.cuh", "sv_ptx.cuh") + [
+CACHE_SOURCES = _csrc("spec_cache.cu")
+CACHE_DEPS = CACHE_SOURCES + _csrc("sc_common.cuh", "sc_attend.cuh", "sc_store.cuh", "sv_ptx.cuh") + [
     HEADER, os.path.join(ROOT, "include", "spec_cache.h")]
 
 NVCC_FLAGS = [
@@ -47,26 +44,18 @@ def up_to_date(lib: str = LIB, deps=None) -> bool:
     return all(os.path.getmtime(p) <= t for p in (DEPS if deps is None else deps))
 
 
-def _link(lib: str, sources, extra) -> None:
-    """One nvcc for each source, side by side, then one to link them."""
-    with tempfile.TemporaryDirectory() as tmp:
-        objects, running = [], []
-        for i, (src, flags) in enumerate(sources):
-            objects.append(os.path.join(tmp, f"{i}.o"))
-            running.append(subprocess.Popen([nvcc()] + NVCC_FLAGS + extra + flags + ["-c", "-o", objects[-1], src]))
-        if any([p.wait() for p in running]):
-            raise RuntimeError(f"building {os.path.basename(lib)} failed")
-        subprocess.run([nvcc()] + NVCC_FLAGS + ["-o", lib + ".tmp"] + objects, check=True)
-    os.replace(lib + ".tmp", lib)
-
-
 def build(force: bool = False, verbose: bool = False) -> str:
     """Build what is out of date; returns the path of ``libspec_verify.so``."""
-    extra = ["-Xptxas", "-v"] if verbose else []
-    if force or not up_to_date():
-        _link(LIB, [(src, []) for src in SOURCES], extra)
-    if force or not up_to_date(CACHE_LIB, CACHE_DEPS):
-        _link(CACHE_LIB, CACHE_SOURCES, extra)
+    running = []
+    for lib, sources, deps in ((LIB, SOURCES, DEPS), (CACHE_LIB, CACHE_SOURCES, CACHE_DEPS)):
+        if not force and up_to_date(lib, deps):
+            continue
+        cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-o", lib + ".tmp"] + sources
+        running.append((lib, subprocess.Popen(cmd)))
+    if any([p.wait() for _, p in running]):
+        raise RuntimeError("nvcc failed")
+    for lib, _ in running:
+        os.replace(lib + ".tmp", lib)
     return LIB
 
 

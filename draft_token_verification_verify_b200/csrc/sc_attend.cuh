@@ -3,22 +3,26 @@
 // For one sequence and key/value head the rows are the n positions x the
 // group's query heads.  A cached key row stands for zero + scale * code, so
 //   q . k = scale * (q . code) + zero * sum(q)
-// and the codes go to the tensor cores as they are; a cached value row is
-// folded into the softmax weight, p' = p * scale, with codes centred to
-// code - 8 (exact) and sum p (zero + 8 scale) added at the end.
+// and the codes go to the tensor cores as they are (as subnormals, a mask
+// each); a cached value row is folded into the softmax weight, p' = p * scale,
+// and sum p (zero + 8 scale) less 8 of the rounded weights is added at the end,
+// so that a weight's rounding meets code - 8.
 //
-// K_attend<DT, D>: 16 rows a block (m16n8k16 MMAs), four warps a CTA, each
-// warp on its own tiles of 64 tokens with its own ring of bulk copies, no
-// barrier between the warps until their (max, sum, output) are merged at the
-// end of a segment.  The fragment order is chosen so that a lane's operands
-// are contiguous in the block: 16 (8) bytes of a key row hold the lane's share
-// of the whole dot product, 8 bytes of a value row its 16 tokens.
+// K_attend: a warp takes 16 rows (m16n8k16 MMAs) and tiles of 64 tokens, with a
+// ring of bulk copies of its own; there is no barrier between the warps until
+// the (maximum, sum, output) of a segment's four are merged.  The fragment order
+// is chosen so that a lane's operands are contiguous in the block: 16 (8) bytes
+// of a key row hold the lane's share of the whole dot product, 8 bytes of a
+// value row its 16 tokens.  The reference maximum of a row is not moved until a
+// score passes it by 2^8, so almost no tile touches the accumulated output.
 //
 // The work: a segment is (sequence, head, block of 16 rows) and has
 // ceil(len / 64) tiles of the cache and ceil(n / 64) units of scored
-// positions.  The segments' tiles in a row are cut into equal ranges, one for
-// each CTA of a single wave; a segment that is cut leaves partial sums that
-// K_join adds in the order of the parts.
+// positions.  CTAs come in groups, one for each of up to SC_LANES row blocks;
+// the segments' units in a row are cut into equal ranges, one for each group of
+// a single wave, so that a group's CTAs walk the same tiles side by side and
+// all but the first find them in L2.  A segment that is cut leaves partial sums
+// that K_join adds in the order of the parts.
 #pragma once
 
 #include "sc_common.cuh"
@@ -28,6 +32,7 @@ namespace sv {
 constexpr int SC_WARPS = 4;
 constexpr int SC_NT = SC_WARPS * 32;
 constexpr int SC_ROWS = 16;   // rows of a block
+constexpr int SC_LANES = 32;      // row blocks side by side at most
 constexpr int SC_MIN_TILES = 4;  // tiles of a CTA's range at least
 
 struct AttendParams {
@@ -38,7 +43,9 @@ struct AttendParams {
     const int32_t* parents;
     long long q_stride, kv_stride;  // elements between tokens
     int B, n, q_heads, group;
-    int rows, row_blocks;  // n * group, in blocks of SC_ROWS (or the tensor-memory kernel's width)
+    int rows;           // n * group
+    int lanes, passes;  // row blocks of a group of CTAs, and times it walks a head: block pass * lanes + lane
+    int cut;            // groups of CTAs that share the units
     int whole;  // a CTA takes one whole segment: nothing is cut, and there is no K_join (and no status)
     float scale;
     void* out;
@@ -46,7 +53,7 @@ struct AttendParams {
     // workspace
     float* part_o;   // [grid][2][rows of a block][D]
     float2* part_ml; // [grid][2][rows of a block]
-    int4* desc;      // [grid]: {segment cut here that begins in this CTA: b, head * row_blocks + block, parts, error}
+    int4* desc;      // [grid]: {segment cut here that begins in this CTA: b, head * passes + pass, parts, error}
     unsigned long long timeout_ns;
     int test_hook;
     int32_t* out_status;
@@ -58,43 +65,41 @@ __device__ __forceinline__ int sc_len(const AttendParams& P, int b, bool* bad) {
     *bad = len > sc_capacity(P.c);
     return (len < 0 || *bad) ? 0 : len;
 }
-template <int TILE>
 __device__ __forceinline__ int sc_new_units(const AttendParams& P) {
-    return P.k_new ? (P.n + TILE - 1) / TILE : 0;
+    return P.k_new ? (P.n + SC_BLOCK - 1) / SC_BLOCK : 0;
 }
-template <int TILE>
 __device__ __forceinline__ int sc_units(const AttendParams& P, int b) {
     bool bad;
-    const int u = (sc_len(P, b, &bad) + TILE - 1) / TILE + sc_new_units<TILE>(P);
+    const int u = (sc_len(P, b, &bad) + SC_BLOCK - 1) / SC_BLOCK + sc_new_units(P);
     return u > 0 ? u : 1;
 }
 
-// A CTA's range of the segments' units, found by all its threads.
+// A group's range of the segments' units, found by all its threads.
 struct Range {
-    long long total, chunk, g0, g1;  // units in all; of a CTA; this CTA's
+    long long total, chunk, g0, g1;  // units in all; of a group; this group's
     int b;                           // sequence that holds g0
     long long before;                // units before that sequence
 };
 
-template <int NT, int TILE>
-__device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) {
+template <int NT>
+__device__ __forceinline__ Range sc_range(const AttendParams& P, int index) {
     __shared__ long long scan[NT / 32];
     __shared__ long long found[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (P.whole) {  // (not a range of units: the segment's number)
-        const int segs = P.c.kv_heads * P.row_blocks;
+        const int segs = P.c.kv_heads * P.passes;
         Range r;
-        r.b = static_cast<int>(blockIdx.x) / segs;
-        r.g0 = blockIdx.x - r.b * segs;
+        r.b = index / segs;
+        r.g0 = index - r.b * segs;
         r.g1 = r.g0 + 1;
         r.total = r.chunk = r.before = 0;
         return r;
     }
     const int per = (P.B + NT - 1) / NT;
-    const long long segs = static_cast<long long>(P.c.kv_heads) * P.row_blocks;
+    const long long segs = static_cast<long long>(P.c.kv_heads) * P.passes;
     long long mine = 0;
 #pragma unroll 1
-    for (int b = tid * per; b < (tid + 1) * per && b < P.B; ++b) mine += sc_units<TILE>(P, b);
+    for (int b = tid * per; b < (tid + 1) * per && b < P.B; ++b) mine += sc_units(P, b);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -112,16 +117,16 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) 
     Range r;
     r.total = total * segs;
     // (rounded up, or one more: a double's error never makes the ranges too short)
-    r.chunk = static_cast<long long>(static_cast<double>(r.total) / gridDim.x) + 1;
-    if (r.chunk < min_units) r.chunk = min_units;
-    r.g0 = r.chunk * blockIdx.x;
+    r.chunk = static_cast<long long>(static_cast<double>(r.total) / P.cut) + 1;
+    if (r.chunk < SC_MIN_TILES) r.chunk = SC_MIN_TILES;
+    r.g0 = r.chunk * index;
     r.g1 = r.g0 + r.chunk < r.total ? r.g0 + r.chunk : r.total;
     long long at = (base + incl - mine) * segs;
     if (r.g0 < r.g1 && r.g0 >= at && r.g0 < at + mine * segs) {
         int b = tid * per;
 #pragma unroll 1
         for (;; ++b) {
-            const long long u = sc_units<TILE>(P, b) * segs;
+            const long long u = sc_units(P, b) * segs;
             if (r.g0 < at + u) break;
             at += u;
         }
@@ -136,9 +141,8 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int min_units) 
 }
 
 // A walk over the parts of segments in a CTA's range.
-template <int TILE>
 struct Walk {
-    int b, hr;       // sequence; head * row_blocks + row block
+    int b, hr;       // sequence; head * passes + pass
     int units, len;  // of the sequence
     int u0, u1;      // the range's share of the segment's units: [u0, u1)
     int left;        // units of the range behind this part
@@ -150,7 +154,7 @@ struct Walk {
         bool above;
         len = __shfl_sync(0xffffffffu, sc_len(P, b, &above), 0);
         bad = __any_sync(0xffffffffu, above);
-        units = (len + TILE - 1) / TILE + sc_new_units<TILE>(P);
+        units = (len + SC_BLOCK - 1) / SC_BLOCK + sc_new_units(P);
         if (units == 0) units = 1;
     }
     __device__ __forceinline__ void begin(const AttendParams& P, const Range& r) {
@@ -172,7 +176,7 @@ struct Walk {
     // The next segment; false behind the range.
     __device__ __forceinline__ bool next(const AttendParams& P) {
         if (left <= 0) return false;
-        if (++hr == P.c.kv_heads * P.row_blocks) {
+        if (++hr == P.c.kv_heads * P.passes) {
             hr = 0;
             ++b;
             sequence(P);
@@ -184,7 +188,7 @@ struct Walk {
     }
     // Whether this part is the whole segment.
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
-    // CTAs that hold parts of a segment begun here and cut by the range's end.
+    // Groups that hold parts of a segment begun here and cut by the range's end.
     __device__ __forceinline__ int parts(int chunk) const { return 1 + (units - u1 + chunk - 1) / chunk; }
 };
 
@@ -194,33 +198,31 @@ __device__ __forceinline__ size_t sc_out_row(const AttendParams& P, int b, int h
     return (static_cast<size_t>(b) * P.n + node) * P.q_heads + head * P.group + g;
 }
 
-template <int D, int MB>
+template <int D>
 struct AttendSmem {
-    static constexpr int GROUPS = SC_WARPS / MB;  // warps of a group share its tiles, 16 rows each
-    static constexpr int STAGES = MB == 1 ? 2 : MB == 2 ? 4 : 8;
-    static constexpr int ROWS = SC_ROWS * MB;     // of the CTA
+    static constexpr int STAGES = 2;  // tiles in flight for each warp
     // Blocks of a tile lie `bstride` bytes apart: shorter blocks are padded so
     // that the four quarter-tiles of a value read fall into different banks.
     static constexpr int TILE = 2 * sc_half_bytes<D>(SC_BLOCK) + 128;
-    static constexpr int RING = GROUPS * STAGES * TILE;
+    static constexpr int RING = SC_WARPS * STAGES * TILE;
     static constexpr int MERGE_ROW = D + 4;  // floats
     static constexpr int MERGE = SC_ROWS * MERGE_ROW * 4;  // a warp's output, or its staged value rows
     static constexpr int OFF_ML = RING + SC_WARPS * MERGE;
     static constexpr int OFF_PAR = OFF_ML + SC_WARPS * SC_ROWS * 8;  // float [warps][32 token pairs][8]
-    static constexpr int OFF_BAD = OFF_PAR + SC_WARPS * 1024;        // int [GROUPS][16]: segments with a bad page
-    static constexpr int OFF_BAR = OFF_BAD + GROUPS * 64;
-    static constexpr int BYTES = OFF_BAR + 2 * GROUPS * STAGES * 8;
+    static constexpr int OFF_BAD = OFF_PAR + SC_WARPS * 1024;        // int [warps][16]: segments with a bad page
+    static constexpr int OFF_BAR = OFF_BAD + SC_WARPS * 64;
+    static constexpr int BYTES = OFF_BAR + SC_WARPS * STAGES * 8;
     static_assert(SC_ROWS * (D + 8) * 2 <= MERGE, "staged value rows fit the merge buffer");
     static_assert(OFF_BAR % 8 == 0 && 2 * (BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
-template <int DT, int D, int MB>
+template <int DT, int D>
 __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_constant__ AttendParams P) {
     using Ty = SC<DT>;
-    using Sm = AttendSmem<D, MB>;
+    using Sm = AttendSmem<D>;
     using T = typename Ty::T;
     constexpr unsigned ALL = 0xffffffffu;
-    constexpr int G = Sm::GROUPS, STAGES = Sm::STAGES;
+    constexpr int STAGES = Sm::STAGES;
     constexpr int KS = D / 16;   // k-steps of a dot product
     constexpr int KW = D / 32;   // 32-bit words of a lane's share of a key row
     constexpr int NV = D / 8;    // n-tiles of the output
@@ -228,43 +230,39 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     // (the broadcast tells the compiler that a warp works as one)
     const int tid = threadIdx.x, warp = __shfl_sync(ALL, tid >> 5, 0), lane = tid & 31;
     const int r8 = lane >> 2, q4 = lane & 3;
-    const int group = warp / MB, mb = warp % MB;
-    unsigned char* ring = sc_raw + group * STAGES * Sm::TILE;
+    const int index = blockIdx.x / P.lanes, row_lane = blockIdx.x - index * P.lanes;  // group, and place in it
+    unsigned char* ring = sc_raw + warp * STAGES * Sm::TILE;
     float* merge = reinterpret_cast<float*>(sc_raw + Sm::RING + warp * Sm::MERGE);
     float2* ml = reinterpret_cast<float2*>(sc_raw + Sm::OFF_ML);
     ulonglong2* par_s = reinterpret_cast<ulonglong2*>(sc_raw + Sm::OFF_PAR + warp * 1024);
-    volatile int* bad_s = reinterpret_cast<int*>(sc_raw + Sm::OFF_BAD) + group * 16;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sc_raw + Sm::OFF_BAR) + group * STAGES;
-    uint64_t* empty = full + G * STAGES;  // (MB > 1: the group's warps have read a stage)
+    volatile int* bad_s = reinterpret_cast<int*>(sc_raw + Sm::OFF_BAD) + warp * 16;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sc_raw + Sm::OFF_BAR) + warp * STAGES;
     const CacheView& c = P.c;
     const float nan = __int_as_float(0x7fffffff);
 
     pdl_launch_dependents();
-    const Range R = sc_range<SC_NT, SC_BLOCK>(P, SC_MIN_TILES);
+    const Range R = sc_range<SC_NT>(P, index);
     bool error = false;
     if (tid == 0 && !P.whole) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (R.g0 >= R.g1) return;
-    if (mb == 0 && lane == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], MB);
-        }
+    if (lane == 0) {
+        for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
     }
-    if (mb == 0 && lane < 16) bad_s[lane] = 0;
-    __syncthreads();
+    if (lane < 16) bad_s[lane] = 0;
+    __syncwarp();
 
     const int nb = SC_BLOCK >> c.log2_block;  // blocks of a tile
     const uint32_t bbytes = 2 * sc_half_bytes<D>(c.block);
     const uint32_t bstride = bbytes + (nb == 1 ? 0 : nb == 2 ? 64 : 32);
     const float sl = P.scale * SC_LOG2E;
 
-    // ---- the copies of a group, by its first warp: STAGES tiles ahead ----
+    // ---- this warp's copies, STAGES tiles ahead ----
     const size_t block_bytes = 2 * sc_half_bytes<D>(c.block);
     const size_t head_bytes = block_bytes * (c.page_size >> c.log2_block), page_bytes = head_bytes * c.kv_heads;
-    Walk<SC_BLOCK> iw;
+    Walk iw;
     iw.begin(P, R);
-    iw.u = iw.u0 + group;
+    iw.u = iw.u0 + warp;
     bool more = true;
     int iw_end = 0, iw_seg = 0;  // behind the part's cache tiles; segments so far
     int ahead_id = 0, issued = 0, used = 0;
@@ -274,7 +272,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         const int tiles = (iw.len + SC_BLOCK - 1) / SC_BLOCK;
         iw_end = iw.u1 < tiles ? iw.u1 : tiles;
         table = c.table + static_cast<size_t>(iw.b) * c.max_pages;
-        ahead = c.pages + head_bytes * (iw.hr / P.row_blocks);
+        ahead = c.pages + head_bytes * (iw.hr / P.passes);
     };
     part();
     // Fetches the page of the next cache tile (at or behind iw.u); lane j that of
@@ -284,7 +282,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         while (iw.u >= iw_end) {
             if (!(more = iw.next(P))) return;
             ++iw_seg;
-            iw.u = iw.u0 + group;
+            iw.u = iw.u0 + warp;
             part();
         }
         const int t = iw.u * SC_BLOCK + (lane << c.log2_block);
@@ -293,10 +291,6 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     auto issue = [&]() {
         if (!more || error) return;
         const int s = issued % STAGES;
-        if (MB > 1 && issued >= STAGES && !sc_wait(&empty[s], ((issued / STAGES) - 1) & 1, P.timeout_ns)) {
-            error = true;
-            return;
-        }
         unsigned char* dst = ring + s * Sm::TILE;
         if (nb == 1) {
             const int id = __shfl_sync(ALL, ahead_id, 0);
@@ -321,14 +315,12 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         }
         __syncwarp();
         ++issued;
-        iw.u += G;
+        iw.u += SC_WARPS;
         fetch();
     };
-    if (mb == 0) {
-        fetch();
+    fetch();
 #pragma unroll 1
-        for (int s = 0; s < (MB == 1 ? STAGES : STAGES - 1); ++s) issue();
-    }
+    for (int s = 0; s < STAGES; ++s) issue();
 
     // What a code's product and a weight are multiplied by.
     const float k_code = DT == 0 ? SC_2P69 : 16777216.f;
@@ -344,11 +336,11 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     const uint32_t half_bytes = sc_half_bytes<D>(Tb), v_step = 8 * (Tb / 2);
 
     int seg = 0;  // segments so far
-    Walk<SC_BLOCK> w;
+    Walk w;
     w.begin(P, R);
 #pragma unroll 1
     for (bool go = true; go; go = w.next(P)) {
-        const int head = w.hr / P.row_blocks, row0 = (w.hr % P.row_blocks) * Sm::ROWS + mb * SC_ROWS;
+        const int head = w.hr / P.passes, row0 = ((w.hr - head * P.passes) * P.lanes + row_lane) * SC_ROWS;
         // ---- this segment's queries, in fragment order ----
         uint32_t qa[KS][4];
         float qs[2] = {0.f, 0.f};
@@ -426,10 +418,9 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         };
 
 #pragma unroll 1
-        for (int u = w.u0 + group; u < w.u1; u += G) {
+        for (int u = w.u0 + warp; u < w.u1; u += SC_WARPS) {
             if (u * SC_BLOCK < w.len) {
                 // ---- a tile of 64 cached tokens ----
-                if (MB > 1 && mb == 0) issue();  // into the stage of the tile before this one
                 const int s = used % STAGES;
                 if (error || !sc_wait(&full[s], (used / STAGES) & 1, P.timeout_ns)) {
                     error = true;  // nothing more is waited for
@@ -568,11 +559,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                     for (int k = 0; k < 4; ++k) sc_mma<0>(o8, pa[k], 0x00080008u, 0x00800080u);
                 }
                 __syncwarp();
-                if constexpr (MB == 1) {
-                    issue();  // into the stage just read
-                } else {
-                    if (lane == 0) sc_arrive(&empty[s]);
-                }
+                issue();  // into the stage just read
             } else if (P.k_new) {
                 // ---- up to 64 of the scored positions, 16 at a time ----
                 const int ub = (u - (w.len + SC_BLOCK - 1) / SC_BLOCK) * SC_BLOCK;
@@ -732,7 +719,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
 
         if (__any_sync(ALL, bad_s[seg & 15])) poison();  // a page out of range
         ++seg;
-        // ---- merge the groups: 16 rows of (reference, sum, output) a warp ----
+        // ---- merge the warps: 16 rows of (reference, sum, output) each ----
         const float os = DT == 0 ? SC_2P69 : 1.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -756,30 +743,28 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         const bool whole = w.whole();
         const int slot = blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0);
         const float* all = reinterpret_cast<const float*>(sc_raw + Sm::RING);
-        constexpr int PER = SC_NT / Sm::ROWS;  // threads of a row
+        constexpr int PER = SC_NT / SC_ROWS;  // threads of a row
         const int r = tid / PER, cpart = tid % PER;
-        const int first = (r / SC_ROWS), r16 = r % SC_ROWS;  // warps first, first + MB, ... hold the row
-        float M = SC_NEG_INF, L = 0.f, wt[G];
+        float M = SC_NEG_INF, L = 0.f, wt[SC_WARPS];
 #pragma unroll
-        for (int i = 0; i < G; ++i) M = fmaxf(M, ml[(first + i * MB) * SC_ROWS + r16].x);
+        for (int i = 0; i < SC_WARPS; ++i) M = fmaxf(M, ml[i * SC_ROWS + r].x);
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-            const float2 v = ml[(first + i * MB) * SC_ROWS + r16];
+        for (int i = 0; i < SC_WARPS; ++i) {
+            const float2 v = ml[i * SC_ROWS + r];
             wt[i] = v.x == SC_NEG_INF ? 0.f : ex2(v.x - M);
             L += v.x == SC_NEG_INF ? v.y : v.y * wt[i];  // (without a reference the sum is 0 or NaN)
         }
-        const int row = (w.hr % P.row_blocks) * Sm::ROWS + r;
+        const int row = row0 + r;
         const float norm = L != L ? nan : !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
         if (row < P.rows || !whole) {
             const size_t orow = whole ? sc_out_row(P, w.b, head, row) : 0;
-#pragma unroll 4
+#pragma unroll
             for (int i = 0; i < D / (4 * PER); ++i) {
                 const int d = (i * PER + cpart) * 4;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    const float4 v = *reinterpret_cast<const float4*>(all + (first + k * MB) * (Sm::MERGE / 4) +
-                                                                      r16 * Sm::MERGE_ROW + d);
+                for (int k = 0; k < SC_WARPS; ++k) {
+                    const float4 v = *reinterpret_cast<const float4*>(all + k * (Sm::MERGE / 4) + r * Sm::MERGE_ROW + d);
                     a.x = fmaf(wt[k], v.x, a.x);
                     a.y = fmaf(wt[k], v.y, a.y);
                     a.z = fmaf(wt[k], v.z, a.z);
@@ -790,69 +775,65 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
                     const uint2 y = make_uint2(Ty::pack(a.x, a.y), Ty::pack(a.z, a.w));
                     *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + orow * D + d) = y;
                 } else {
-                    *reinterpret_cast<float4*>(P.part_o + (static_cast<size_t>(slot) * Sm::ROWS + r) * D + d) = a;
+                    *reinterpret_cast<float4*>(P.part_o + (static_cast<size_t>(slot) * SC_ROWS + r) * D + d) = a;
                 }
             }
             if (cpart == 0) {
                 if (!whole)
-                    P.part_ml[static_cast<size_t>(slot) * Sm::ROWS + r] = make_float2(M, L);
+                    P.part_ml[static_cast<size_t>(slot) * SC_ROWS + r] = make_float2(M, L);
                 else if (P.out_lse)
                     P.out_lse[orow] = L == 0.f ? SC_NEG_INF : (M + log2f(L)) * SC_LN2;
             }
         }
         if (tid == 0 && w.u0 == 0 && !whole)
             P.desc[blockIdx.x] = make_int4(w.b, w.hr, w.parts(static_cast<int>(R.chunk)), 0);
-        if (mb == 0 && lane == 0) bad_s[(seg - 1) & 15] = 0;
+        if (lane == 0) bad_s[(seg - 1) & 15] = 0;
         __syncthreads();  // the merge buffers are free
     }
     // no copy may land after the CTA is gone (after an error some are still under way)
-    if (mb == 0) {
 #pragma unroll 1
-        for (; used < issued; ++used)
-            if (!sc_wait(&full[used % STAGES], (used / STAGES) & 1, P.timeout_ns)) error = true;
-    }
+    for (; used < issued; ++used)
+        if (!sc_wait(&full[used % STAGES], (used / STAGES) & 1, P.timeout_ns)) error = true;
     if (error && lane == 0 && !P.whole) P.desc[blockIdx.x].w = 1;
 }
 
 // K_join: block (i, j) adds the parts of the segment that is cut in CTA i and
-// begins there, rows j, j + gridDim.y, ..., in the order of the parts.
+// begins there, rows 4 j .. 4 j + 3, a warp each, in the order of the parts.
 constexpr int SC_JOIN_NT = 128;
 
 template <int DT, int D>
-__global__ void __launch_bounds__(SC_JOIN_NT) sc_join_kernel(const __grid_constant__ AttendParams P, int grid,
-                                                            int block_rows) {
+__global__ void __launch_bounds__(SC_JOIN_NT) sc_join_kernel(const __grid_constant__ AttendParams P) {
     using Ty = SC<DT>;
     pdl_wait_primary();
     if (blockIdx.x == 0 && blockIdx.y == 0 && P.out_status) {
         int err = 0;
-        for (int i = threadIdx.x; i < grid; i += SC_JOIN_NT) err |= P.desc[i].w;
+        for (int i = threadIdx.x; i < gridDim.x; i += SC_JOIN_NT) err |= P.desc[i].w;
         err = __syncthreads_or(err);
         if (threadIdx.x == 0) *P.out_status = err ? -4 : 0;
     }
     const int4 d = P.desc[blockIdx.x];
     if (d.x < 0 || d.z == 0) return;
-    const int head = d.y / P.row_blocks, row0 = (d.y % P.row_blocks) * block_rows;
+    const int head = d.y / P.passes;
+    const int row0 = ((d.y - head * P.passes) * P.lanes + static_cast<int>(blockIdx.x) % P.lanes) * SC_ROWS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int V = D / 32;  // outputs of a lane
-    for (int r = blockIdx.y * (SC_JOIN_NT / 32) + warp; r < block_rows && row0 + r < P.rows;
-         r += gridDim.y * (SC_JOIN_NT / 32)) {
+    const int r = blockIdx.y * (SC_JOIN_NT / 32) + warp;
+    if (row0 + r < P.rows) {
+        // part p lies in the p-th next group's CTA of the same lane
+        auto slot = [&](int p) { return (blockIdx.x + p * P.lanes) * 2 + (p == 0 ? 1 : 0); };
         float M = SC_NEG_INF;
-        for (int p = lane; p < d.z; p += 32) {
-            const int slot = (blockIdx.x + p) * 2 + (p == 0 ? 1 : 0);
-            M = fmaxf(M, P.part_ml[static_cast<size_t>(slot) * block_rows + r].x);
-        }
+        for (int p = lane; p < d.z; p += 32) M = fmaxf(M, P.part_ml[static_cast<size_t>(slot(p)) * SC_ROWS + r].x);
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
         float L = 0.f, a[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) a[i] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int p = 0; p < d.z; ++p) {
-            const int slot = (blockIdx.x + p) * 2 + (p == 0 ? 1 : 0);
-            const size_t at = static_cast<size_t>(slot) * block_rows + r;
+            const size_t at = static_cast<size_t>(slot(p)) * SC_ROWS + r;
             const float2 v = P.part_ml[at];
             const float wt = v.x == SC_NEG_INF ? 0.f : ex2(v.x - M);
-            L += v.x == SC_NEG_INF ? v.y : v.y * wt;  // (without a maximum the sum is 0 or NaN)
+            L += v.x == SC_NEG_INF ? v.y : v.y * wt;  // (without a reference the sum is 0 or NaN)
             const float* src = P.part_o + at * D + lane * V;
 #pragma unroll
             for (int i = 0; i < V; ++i) a[i] = fmaf(wt, src[i], a[i]);

@@ -9,7 +9,6 @@
 
 #include "../../include/spec_cache.h"
 #include "sc_attend.cuh"
-#include "sc_plan.h"
 #include "sc_store.cuh"
 
 namespace {
@@ -89,54 +88,52 @@ sv_status_t check_cache(const sv_cache_t* c, sv::CacheView* v, int* dt) {
 
 // ---- the attention's plan ---------------------------------------------------------
 
-using JoinFn = void (*)(sv::AttendParams, int, int);
+using AttendFn = void (*)(sv::AttendParams);
+
+AttendFn pick_attend(int dt, int D) {
+    if (D == 64) return dt ? sv::sc_attend_kernel<1, 64> : sv::sc_attend_kernel<0, 64>;
+    return dt ? sv::sc_attend_kernel<1, 128> : sv::sc_attend_kernel<0, 128>;
+}
+AttendFn pick_join(int dt, int D) {
+    if (D == 64) return dt ? sv::sc_join_kernel<1, 64> : sv::sc_join_kernel<0, 64>;
+    return dt ? sv::sc_join_kernel<1, 128> : sv::sc_join_kernel<0, 128>;
+}
+int attend_smem(int D) { return D == 64 ? sv::AttendSmem<64>::BYTES : sv::AttendSmem<128>::BYTES; }
 
 struct Plan {
-    sv::AttendKernel k;
-    int grid = 0, row_blocks = 0;
+    int lanes = 0, passes = 0, cut = 0, grid = 0;
     size_t off_ml = 0, off_desc = 0, bytes = 0;
 };
 
-sv::AttendKernel pick_attend(int dt, int D, int rows) {
-    if (D == 64) return dt ? sv::attend_kernel<1, 64>(rows) : sv::attend_kernel<0, 64>(rows);
-    return dt ? sv::attend_kernel<1, 128>(rows) : sv::attend_kernel<0, 128>(rows);
-}
-
-// The kernel and its launch shape.  Rows beyond SC_MOST_ROWS go in equal blocks.
-bool make_plan(const DeviceInfo& d, int B, int n, int q_heads, int kv_heads, int D, int dt, Plan* p) {
+// The launch shape: two CTAs an SM in a single wave, in groups of one for each row block.
+bool make_plan(const DeviceInfo& d, int B, int n, int q_heads, int kv_heads, int D, Plan* p) {
     const long long rows = static_cast<long long>(n) * (q_heads / kv_heads);
     if (rows > (1 << 24)) return false;
-    p->k = pick_attend(dt, D, static_cast<int>(ceil_div(rows, ceil_div(rows, sv::SC_MOST_ROWS))));
-    p->row_blocks = static_cast<int>(ceil_div(rows, p->k.block_rows));
-    p->grid = p->k.per_sm * d.sms;
-    const size_t parts = static_cast<size_t>(p->grid) * 2 * p->k.block_rows;
+    const long long blocks = ceil_div(rows, sv::SC_ROWS);
+    p->passes = static_cast<int>(ceil_div(blocks, sv::SC_LANES));
+    p->lanes = static_cast<int>(ceil_div(blocks, p->passes));
+    p->cut = 2 * d.sms / p->lanes;
+    p->grid = p->cut * p->lanes;
+    const size_t parts = static_cast<size_t>(p->grid) * 2 * sv::SC_ROWS;
     p->off_ml = round_up(parts * D * sizeof(float), 256);
     p->off_desc = p->off_ml + round_up(parts * sizeof(float2), 256);
     p->bytes = p->off_desc + round_up(static_cast<size_t>(p->grid) * sizeof(int4), 256);
-    return static_cast<long long>(B) * kv_heads * p->row_blocks < (1LL << 31);
+    return p->cut > 0 && static_cast<long long>(B) * kv_heads * p->passes * p->lanes < (1LL << 31);
 }
 
 bool attend_sizes_ok(int B, int n, int q_heads, int kv_heads) {
     return B > 0 && n >= 1 && n <= sv::SC_MAX_NODES && kv_heads > 0 && q_heads > 0 && q_heads % kv_heads == 0;
 }
 
-JoinFn pick_join(int dt, int D) {
-    if (D == 64) return dt ? sv::sc_join_kernel<1, 64> : sv::sc_join_kernel<0, 64>;
-    return dt ? sv::sc_join_kernel<1, 128> : sv::sc_join_kernel<0, 128>;
-}
-
 sv_status_t set_attrs(int dev) {
     std::call_once(g_attr_once[dev], [dev] {
         cudaError_t e = cudaSuccess;
         for (int dt = 0; dt < 2; ++dt)
-            for (int D = 64; D <= 128; D += 64)
-                for (int rows = 1; rows <= sv::SC_MOST_ROWS;) {
-                    const sv::AttendKernel k = pick_attend(dt, D, rows);
-                    rows = k.block_rows + 1;
-                    const cudaError_t x = cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn),
-                                                               cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-                    if (x != cudaSuccess) e = x;
-                }
+            for (int D = 64; D <= 128; D += 64) {
+                const cudaError_t x = cudaFuncSetAttribute(reinterpret_cast<const void*>(pick_attend(dt, D)),
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem(D));
+                if (x != cudaSuccess) e = x;
+            }
         if (e != cudaSuccess) cudaGetLastError();
         g_attr_err[dev] = e;
     });
@@ -161,7 +158,7 @@ size_t spec_cache_attend_workspace_size(int B, int n, int q_heads, int kv_heads,
     int dev = 0;
     const DeviceInfo* d = device_info(&dev);
     Plan p;
-    return d && make_plan(*d, B, n, q_heads, kv_heads, head_dim, 0, &p) ? p.bytes : 0;
+    return d && make_plan(*d, B, n, q_heads, kv_heads, head_dim, &p) ? p.bytes : 0;
 }
 
 sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_new, const void* v_new,
@@ -187,7 +184,7 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     const DeviceInfo* info = device_info(&dev);
     if (!info) return SV_ERR_UNSUPPORTED;
     Plan plan;
-    if (!make_plan(*info, B, n, q_heads, cache->kv_heads, D, dt, &plan)) return SV_ERR_UNSUPPORTED;
+    if (!make_plan(*info, B, n, q_heads, cache->kv_heads, D, &plan)) return SV_ERR_UNSUPPORTED;
     if (workspace_bytes < plan.bytes) return SV_ERR_INVALID_ARG;
     const sv_status_t sa = set_attrs(dev);
     if (sa != SV_OK) return sa;
@@ -203,15 +200,15 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     P.q_heads = q_heads;
     P.group = q_heads / cache->kv_heads;
     P.rows = n * P.group;
-    P.row_blocks = plan.row_blocks;
+    P.lanes = plan.lanes;
+    P.passes = plan.passes;
+    P.cut = plan.cut;
     P.scale = scale;
     // Short contexts (by the page table's width, the lengths being on the device): a CTA takes a whole
     // segment, and one launch does.  That costs less than the join up to
     // kWholeTokens a segment.
-    const long long tiles = ceil_div(static_cast<long long>(cache->max_pages) * cache->page_size, plan.k.tile) +
-                            (k_new ? ceil_div(n, plan.k.tile) : 0);
-    P.whole = tiles * plan.k.tile <= kWholeTokens && !out_status;
-    if (P.whole) plan.grid = static_cast<int>(static_cast<long long>(B) * cache->kv_heads * plan.row_blocks);
+    P.whole = static_cast<long long>(cache->max_pages) * cache->page_size + (k_new ? n : 0) <= kWholeTokens && !out_status;
+    if (P.whole) plan.grid = static_cast<int>(static_cast<long long>(B) * cache->kv_heads * plan.passes * plan.lanes);
     P.out = out;
     P.out_lse = out_lse;
     auto* ws = static_cast<unsigned char*>(workspace);
@@ -230,10 +227,10 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(plan.k.threads), 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(plan.k.smem);
+    cfg.blockDim = dim3(sv::SC_NT, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(attend_smem(D));
     cfg.stream = st;
-    sv_status_t r = launched(cudaLaunchKernelEx(&cfg, plan.k.fn, P));
+    sv_status_t r = launched(cudaLaunchKernelEx(&cfg, pick_attend(dt, D), P));
     if (r != SV_OK) return r;
     if (opts && opts->event_stop) {
         r = launched(cudaEventRecord(static_cast<cudaEvent_t>(opts->event_stop), st));
@@ -244,12 +241,12 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     a[0].val.programmaticStreamSerializationAllowed = 1;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), static_cast<unsigned>(plan.k.block_rows / 4), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), sv::SC_ROWS / (sv::SC_JOIN_NT / 32), 1);
     cfg.blockDim = dim3(sv::SC_JOIN_NT, 1, 1);
     cfg.stream = st;
     cfg.attrs = a;
     cfg.numAttrs = 1;
-    return launched(cudaLaunchKernelEx(&cfg, pick_join(dt, D), P, plan.grid, plan.k.block_rows));
+    return launched(cudaLaunchKernelEx(&cfg, pick_join(dt, D), P));
 }
 
 sv_status_t spec_cache_append(const sv_cache_t* cache, const void* k, const void* v, long long kv_stride, int B,
