@@ -209,8 +209,7 @@ struct AttendSmem {
     static constexpr int MERGE = SC_ROWS * MERGE_ROW * 4;  // a warp's output, or its staged value rows
     static constexpr int OFF_ML = RING + SC_WARPS * MERGE;
     static constexpr int OFF_PAR = OFF_ML + SC_WARPS * SC_ROWS * 8;  // float [warps][32 token pairs][8]
-    static constexpr int OFF_BAD = OFF_PAR + SC_WARPS * 1024;        // int [warps][16]: segments with a bad page
-    static constexpr int OFF_BAR = OFF_BAD + SC_WARPS * 64;
+    static constexpr int OFF_BAR = OFF_PAR + SC_WARPS * 1024;
     static constexpr int BYTES = OFF_BAR + SC_WARPS * STAGES * 8;
     static_assert(SC_ROWS * (D + 8) * 2 <= MERGE, "staged value rows fit the merge buffer");
     static_assert(OFF_BAR % 8 == 0 && 2 * (BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -235,7 +234,6 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     float* merge = reinterpret_cast<float*>(sc_raw + Sm::RING + warp * Sm::MERGE);
     float2* ml = reinterpret_cast<float2*>(sc_raw + Sm::OFF_ML);
     ulonglong2* par_s = reinterpret_cast<ulonglong2*>(sc_raw + Sm::OFF_PAR + warp * 1024);
-    volatile int* bad_s = reinterpret_cast<int*>(sc_raw + Sm::OFF_BAD) + warp * 16;
     uint64_t* full = reinterpret_cast<uint64_t*>(sc_raw + Sm::OFF_BAR) + warp * STAGES;
     const CacheView& c = P.c;
     const float nan = __int_as_float(0x7fffffff);
@@ -249,7 +247,6 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
     }
-    if (lane < 16) bad_s[lane] = 0;
     __syncwarp();
 
     const int nb = SC_BLOCK >> c.log2_block;  // blocks of a tile
@@ -264,7 +261,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     iw.begin(P, R);
     iw.u = iw.u0 + warp;
     bool more = true;
-    int iw_end = 0, iw_seg = 0;  // behind the part's cache tiles; segments so far
+    int iw_end = 0;  // behind the part's cache tiles
     int ahead_id = 0, issued = 0, used = 0;
     const unsigned char* ahead = nullptr;  // the tile's first block on a page at 0
     const int32_t* table = nullptr;
@@ -281,12 +278,17 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
 #pragma unroll 1
         while (iw.u >= iw_end) {
             if (!(more = iw.next(P))) return;
-            ++iw_seg;
             iw.u = iw.u0 + warp;
             part();
         }
         const int t = iw.u * SC_BLOCK + (lane << c.log2_block);
         ahead_id = __ldg(table + ((lane < nb && t < iw.len ? t : iw.u * SC_BLOCK) >> c.log2_page));
+    };
+    // Instead of a page out of range: the block's first token, which always counts,
+    // gets NaN for a key's parameters, and with it every row of the segment.
+    auto absent = [&](unsigned char* block) {
+        *reinterpret_cast<uint32_t*>(block + c.block * (D / 2)) = 0x7fff7fffu;
+        fence_proxy_async();  // before the stage's next copy
     };
     auto issue = [&]() {
         if (!more || error) return;
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
             const int id = __shfl_sync(ALL, ahead_id, 0);
             const bool fine = static_cast<unsigned>(id) < static_cast<unsigned>(c.num_pages);
             if (sc_elect()) {
-                if (!fine) bad_s[iw_seg & 15] = 1;
+                if (!fine) absent(dst);
                 mbar_arrive_expect_tx(&full[s], fine || P.test_hook ? bbytes : 0u);
                 if (fine && !P.test_hook)
                     bulk_g2s(dst, ahead + page_bytes * id + block_bytes * ((iw.u * SC_BLOCK & (c.page_size - 1)) / SC_BLOCK),
@@ -305,11 +307,9 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         } else {
             const bool mine = lane < nb && iw.u * SC_BLOCK + (lane << c.log2_block) < iw.len;
             const bool fine = mine && static_cast<unsigned>(ahead_id) < static_cast<unsigned>(c.num_pages);
-            const unsigned got = __ballot_sync(ALL, fine), want = __ballot_sync(ALL, mine);
-            if (lane == 0) {
-                if (got != want) bad_s[iw_seg & 15] = 1;
-                mbar_arrive_expect_tx(&full[s], bbytes * (P.test_hook ? 1 : __popc(got)));
-            }
+            const unsigned got = __ballot_sync(ALL, fine);
+            if (mine && !fine) absent(dst + lane * bstride);
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], bbytes * (P.test_hook ? 1 : __popc(got)));
             __syncwarp();
             if (fine && !P.test_hook) bulk_g2s(dst + lane * bstride, ahead + page_bytes * ahead_id, bbytes, &full[s]);
         }
@@ -335,7 +335,6 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
     const uint32_t v_off = q_blk + sc_half_bytes<D>(Tb) + r8 * (Tb / 2) + (tq & (Tb - 1)) / 2;
     const uint32_t half_bytes = sc_half_bytes<D>(Tb), v_step = 8 * (Tb / 2);
 
-    int seg = 0;  // segments so far
     Walk w;
     w.begin(P, R);
 #pragma unroll 1
@@ -717,8 +716,6 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
             }
         }
 
-        if (__any_sync(ALL, bad_s[seg & 15])) poison();  // a page out of range
-        ++seg;
         // ---- merge the warps: 16 rows of (reference, sum, output) each ----
         const float os = DT == 0 ? SC_2P69 : 1.f;
 #pragma unroll
@@ -787,7 +784,6 @@ __global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_consta
         }
         if (tid == 0 && w.u0 == 0 && !whole)
             P.desc[blockIdx.x] = make_int4(w.b, w.hr, w.parts(static_cast<int>(R.chunk)), 0);
-        if (lane == 0) bad_s[(seg - 1) & 15] = 0;
         __syncthreads();  // the merge buffers are free
     }
     // no copy may land after the CTA is gone (after an error some are still under way)

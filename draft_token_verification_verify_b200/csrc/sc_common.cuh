@@ -126,6 +126,11 @@ constexpr float SC_2P64 = 18446744073709551616.f;
 constexpr float SC_2P60 = 1152921504606846976.f;
 constexpr float SC_2P69 = 590295810358705651712.f;
 
+// Orders this thread's shared-memory accesses before bulk copies that follow.
+__device__ __forceinline__ void fence_proxy_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ void sc_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }

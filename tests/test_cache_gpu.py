@@ -239,6 +239,26 @@ def test_attend_data_errors():
     assert bool(torch.isnan(out[:3]).all())
 
 
+@pytest.mark.parametrize("page,fill", [(64, 0), (64, 30), (16, 0), (16, 30)])
+def test_attend_bad_pages_of_few_sequences(page, fill):
+    """Every tenth sequence is long, the rest leave some warps without a cached tile: a bad page of one of
+    them, far ahead of the segment that is computed, is that sequence's alone."""
+    lens = [290 if b % 10 == 9 else fill for b in range(70)] + [3000]
+    c = Case(lens, page, 2, 64, torch.bfloat16, 64, seed=31)
+    q, k, v = c.tokens(16), c.tokens(2), c.tokens(2)
+    want = c.want(q, k, v)
+    bad = [9, 29, 39, 49, 69]
+    for i, b in enumerate(bad):
+        c.d_table[b, (64 * (3 - i % 4) + 63) // page] = -1 if i % 2 else c.pages.num
+    out, lse = c.attend(q, k, v)
+    fine = ((out - want[0]).abs() <= want[2]).all(-1).all(-1).all(-1)
+    for b in range(len(lens)):
+        if b in bad:
+            assert bool(torch.isnan(out[b]).all()) and bool(torch.isnan(lse[b]).all()), b
+        else:
+            assert bool(fine[b]), b
+
+
 def test_attend_wait_that_runs_out():
     c = Case([200], 64, 1, 128, torch.bfloat16, 2, seed=19)
     q = c.tokens(4)
