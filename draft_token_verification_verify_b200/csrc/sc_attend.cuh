@@ -32,8 +32,15 @@ namespace sv {
 constexpr int SC_WARPS = 4;
 constexpr int SC_NT = SC_WARPS * 32;
 constexpr int SC_ROWS = 16;   // rows of a block
-constexpr int SC_LANES = 32;      // row blocks side by side at most
+constexpr int SC_LANES = 32;  // row blocks side by side at most
 constexpr int SC_MIN_TILES = 4;  // tiles of a CTA's range at least
+
+// CTAs an SM.  The products of 64 dims fit 168 registers a thread, and a third
+// CTA hides more of a tile's latency than it costs: 128 sequences of 6,200 to
+// 9,800 tokens, 32 query and 8 key heads, 4 positions, 239 -> 216 us; 64 trees
+// of 9 nodes on up to 2,300 tokens in fp16, 129 -> 106 us.  Those of 128 dims
+// spill there (317 -> 432 us).
+constexpr int sc_ctas(int D) { return D == 64 ? 3 : 2; }
 
 struct AttendParams {
     CacheView c;
@@ -212,11 +219,11 @@ struct AttendSmem {
     static constexpr int OFF_BAR = OFF_PAR + SC_WARPS * 1024;
     static constexpr int BYTES = OFF_BAR + SC_WARPS * STAGES * 8;
     static_assert(SC_ROWS * (D + 8) * 2 <= MERGE, "staged value rows fit the merge buffer");
-    static_assert(OFF_BAR % 8 == 0 && 2 * (BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
+    static_assert(OFF_BAR % 8 == 0 && sc_ctas(D) * (BYTES + 1024) <= 228 * 1024, "an SM's shared memory");
 };
 
 template <int DT, int D>
-__global__ void __launch_bounds__(SC_NT, 2) sc_attend_kernel(const __grid_constant__ AttendParams P) {
+__global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __grid_constant__ AttendParams P) {
     using Ty = SC<DT>;
     using Sm = AttendSmem<D>;
     using T = typename Ty::T;

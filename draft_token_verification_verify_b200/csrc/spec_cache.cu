@@ -105,14 +105,14 @@ struct Plan {
     size_t off_ml = 0, off_desc = 0, bytes = 0;
 };
 
-// The launch shape: two CTAs an SM in a single wave, in groups of one for each row block.
+// The launch shape: a single wave of sc_ctas(D) CTAs an SM, in groups of one for each row block.
 bool make_plan(const DeviceInfo& d, int B, int n, int q_heads, int kv_heads, int D, Plan* p) {
     const long long rows = static_cast<long long>(n) * (q_heads / kv_heads);
     if (rows > (1 << 24)) return false;
     const long long blocks = ceil_div(rows, sv::SC_ROWS);
     p->passes = static_cast<int>(ceil_div(blocks, sv::SC_LANES));
     p->lanes = static_cast<int>(ceil_div(blocks, p->passes));
-    p->cut = 2 * d.sms / p->lanes;
+    p->cut = sv::sc_ctas(D) * d.sms / p->lanes;
     p->grid = p->cut * p->lanes;
     const size_t parts = static_cast<size_t>(p->grid) * 2 * sv::SC_ROWS;
     p->off_ml = round_up(parts * D * sizeof(float), 256);
