@@ -99,49 +99,51 @@ __device__ __forceinline__ void sc_fold(uint32_t (&x)[16], int l, unsigned mask)
 // The codes of 4 elements as floats: (x - zero) / scale rounded to the nearest
 // whole number, ties to even, as the exact fp32 quotient decides.  The product
 // with the reciprocal is within 1e-5 of that quotient (which stays below 15.1
-// while the scale is a normal number); where it comes that close to a half, or
-// the reciprocal is of no use (NaN), sc_near decides.
-__device__ __noinline__ void sc_near(uint64_t d01, uint64_t d23, float scale, float inv, uint64_t& c01, uint64_t& c23) {
-    float d[4], c[4];
-    f2_unpack(d01, d[0], d[1]);
-    f2_unpack(d23, d[2], d[3]);
-    f2_unpack(c01, c[0], c[1]);
-    f2_unpack(c23, c[2], c[3]);
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        const float e = d[i] * inv - c[i];
-        if (fabsf(e) < 0.49998f) continue;
-        // the half between two codes, and on which side of it the quotient lies (the sign of the fused
-        // difference is exact); too close to tell by that, or no reciprocal: divide
-        const float h = c[i] + (e > 0.f ? 0.5f : -0.5f);
-        const float r = fmaf(-h, scale, d[i]);
-        float x;
-        if (fabsf(r) > 1e-6f * d[i]) {
-            x = r > 0.f ? h + 0.5f : h - 0.5f;
-        } else {
-            x = scale > 0.f ? fminf(rintf(__fdiv_rn(d[i], scale)), 15.f) : 0.f;
-            if (!(x >= 0.f)) x = 0.f;
-        }
-        c[i] = x;
-    }
-    c01 = f2_pack(c[0], c[1]);
-    c23 = f2_pack(c[2], c[3]);
+// while the scale is a normal number).  Where it comes that close to a half
+// (both sides have few bits, so that of 128 elements one often lies on it), the
+// remainder decides: d - code * scale has no rounding error (a multiple of d's
+// last bit and no larger than d), and a quotient that is not a half lies
+// further from one than half its last bit, so that the exact quotient and the
+// rounded one fall on the same side.
+__device__ __forceinline__ void sc_near(float& c, float d, float scale, float half) {
+    const float r = fmaf(-c, scale, d), a = fabsf(r);
+    c += copysignf(a > half ? 0.75f : a == half ? 0.5f : 0.25f, r);
+}
+// ... and where the scale is too small for a reciprocal.
+__device__ __noinline__ float sc_divided(float d, float scale) {
+    const float x = scale > 0.f ? fminf(rintf(__fdiv_rn(d, scale)), 15.f) : 0.f;
+    return x >= 0.f ? x : 0.f;
 }
 __device__ __forceinline__ void sc_codes4(uint64_t x01, uint64_t x23, float zero, float scale, float inv,
                                           uint64_t& c01, uint64_t& c23) {
-    const uint64_t nz = f2_pack(-zero, -zero), i2 = f2_pack(inv, inv);
+    const uint64_t nz = f2_pack(-zero, -zero), i2 = f2_pack(inv, inv), minus = f2_pack(-1.f, -1.f);
     const uint64_t up = f2_pack(12582912.f, 12582912.f), down = f2_pack(-12582912.f, -12582912.f);
     const uint64_t d01 = f2_add(x01, nz), d23 = f2_add(x23, nz);
     const uint64_t q01 = f2_mul(d01, i2), q23 = f2_mul(d23, i2);
     c01 = f2_add(f2_add(q01, up), down);
     c23 = f2_add(f2_add(q23, up), down);
-    float a, b, c, d, e0, e1, e2, e3;
-    f2_unpack(c01, a, b);
-    f2_unpack(c23, c, d);
-    f2_unpack(q01, e0, e1);
-    f2_unpack(q23, e2, e3);
-    const float off = fmaxf(fmaxf(fabsf(e0 - a), fabsf(e1 - b)), fmaxf(fabsf(e2 - c), fabsf(e3 - d)));
-    if (off >= 0.49998f || inv != inv) sc_near(d01, d23, scale, inv, c01, c23);
+    float e0, e1, e2, e3;
+    f2_unpack(f2_fma(c01, minus, q01), e0, e1);
+    f2_unpack(f2_fma(c23, minus, q23), e2, e3);
+    const float off = fmaxf(fmaxf(fabsf(e0), fabsf(e1)), fmaxf(fabsf(e2), fabsf(e3)));
+    if (off >= 0.49998f || inv != inv) {
+        float c[4], d[4];
+        f2_unpack(c01, c[0], c[1]);
+        f2_unpack(c23, c[2], c[3]);
+        f2_unpack(d01, d[0], d[1]);
+        f2_unpack(d23, d[2], d[3]);
+        if (inv == inv) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc_near(c[i], d[i], scale, 0.5f * scale);
+            c01 = f2_add(f2_add(f2_pack(c[0], c[1]), up), down);
+            c23 = f2_add(f2_add(f2_pack(c[2], c[3]), up), down);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = sc_divided(d[i], scale);
+            c01 = f2_pack(c[0], c[1]);
+            c23 = f2_pack(c[2], c[3]);
+        }
+    }
 }
 
 // Low 16 bits: a whole number below 2^16 held in a float.

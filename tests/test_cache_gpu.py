@@ -421,6 +421,30 @@ def test_append_hard_rows(kind):
     assert bool(torch.isnan(rk[0, 8:11]).all()) and bool((rk[0, 0] == 3.0).all())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_halves(kind, D):
+    """Quotients on a half, and as close to one as the types allow (a half less or more a number that is tiny
+    beside the row's minimum), over scales of every mantissa."""
+    T = TYPES[kind]
+    n = 512
+    c = Case([3], 64, 2, D, T, n, seed=8)
+    x = torch.zeros((n, 2, D), dtype=torch.float64)
+    for r in range(n):
+        s = (128 + r % 128) * 2.0 ** (-9 - (r // 128) % 2)
+        x[r, 0] = torch.randint(0, 31, (D,), generator=c.g).double() / 2 * s
+        x[r, 0, :2] = torch.tensor([0.0, 15 * s])
+        zero = -0.5 * s if r % 3 == 0 else -1.5 * s if r % 3 == 1 else -7.5 * s
+        tiny = torch.randint(-8, 9, (D,), generator=c.g).double() * s * 2.0 ** -(20 + r % 7 if T == torch.bfloat16 else 10 + r % 4)
+        x[r, 1] = torch.where(torch.rand(D, generator=c.g) < 0.7, tiny, zero + torch.randint(0, 31, (D,), generator=c.g) / 2 * s)
+        x[r, 1, :2] = torch.tensor([zero, zero + 15 * s])
+    k = x[None].to(T)
+    v = k.flip(1).contiguous()
+    append(c, k, v)
+    expect_append(c, k, v, [range(n)])
+    same_pages(c)
+
+
 def test_append_data_errors():
     lens = [20, 20, 20, 44, 20]
     c = Case(lens, 16, 2, 64, torch.bfloat16, 5, seed=8)
