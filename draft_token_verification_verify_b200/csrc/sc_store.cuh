@@ -1,19 +1,21 @@
 // Writing the 4-bit cache and reading it back.
 //
 // K_append quantises the kept rows behind each sequence's length; K_read
-// expands a range of every sequence.  In both a group of D / 4 lanes (a warp at
-// D = 128, half a warp at D = 64) takes one (sequence, 8 tokens of a block,
-// head) and each lane 4 dims, so that the word of 8 tokens of a value row
-// (values are stored dim by dim) is built, or taken apart, within one lane.
-// Heads are the fastest index of the groups: neighbours read, or write, whole
-// token rows.  Both are bound by the bytes they move; nothing is read twice.
+// expands a range of every sequence.  In both a CTA takes 64 positions (from a
+// multiple of 64) of one (sequence, head).  A group of D / 4 lanes (a warp at
+// D = 128, half a warp at D = 64) takes 8 of them and each lane 4 dims, so that
+// the word of 8 tokens of a value row (values are stored dim by dim) is built,
+// or taken apart, within one lane; the words of the 8 groups meet in shared
+// memory, since those of one group lie a whole row apart.  Nothing is read
+// twice.
 #pragma once
 
 #include "sc_common.cuh"
 
 namespace sv {
 
-constexpr int SC_STORE_NT = 128;
+constexpr int SC_TILE = 64;  // positions of a CTA
+constexpr int sc_store_threads(int D) { return SC_TILE / 8 * (D / 4); }
 
 struct AppendParams {
     const void* k;
@@ -24,7 +26,7 @@ struct AppendParams {
     const int32_t* nodes;       // or null
     int nodes_stride;
     int32_t* out_lens;  // null when a later kernel advances the lengths in place
-    int ngrp;           // groups of 8 positions a sequence's new rows can touch
+    int tiles;          // of 64 positions that a sequence's new rows can touch
 };
 
 struct ReadParams {
@@ -32,7 +34,7 @@ struct ReadParams {
     void* out_k;
     void* out_v;
     int B, n;
-    int ngrp;
+    int tiles;
 };
 
 // min of bf16 / fp16 pairs, NaN if either is.
@@ -146,48 +148,66 @@ __device__ __forceinline__ void sc_codes4(uint64_t x01, uint64_t x23, float zero
     }
 }
 
+// Where a tile's value words lie in shared memory: 8 groups' words of the dim,
+// the rows of 4 dims (128 bytes) rotated so that neither side meets one bank.
+__device__ __forceinline__ int sc_word(int dim, int group) {
+    const int row = dim >> 2;
+    return row * 32 + ((((dim & 3) * 2 + (group >> 2) + row) & 7) << 2) + (group & 3);
+}
+// The 16 bytes a thread moves between them and the blocks: (dim, half of the
+// groups), in the blocks' order.
+template <int D>
+__device__ __forceinline__ void sc_share(int T, int* dim, int* half) {
+    const int t = threadIdx.x;
+    *dim = T == SC_TILE ? t >> 1 : t % D;
+    *half = T == SC_TILE ? t & 1 : t / D;
+}
+// Bits [from, to) of 8.
+__device__ __forceinline__ uint32_t sc_bits8(int from, int to) {
+    from = from > 0 ? from : 0;
+    to = to < 8 ? to : 8;
+    return from < to ? (0xffu >> (8 - to)) & (0xffu << from) : 0u;
+}
+
 // Low 16 bits: a whole number below 2^16 held in a float.
 __device__ __forceinline__ uint32_t sc_bits(float c) { return __float_as_uint(c + 8388608.f); }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, AppendParams P) {
+__global__ void __launch_bounds__(sc_store_threads(D)) sc_append_kernel(CacheView c, AppendParams P) {
     using Ty = SC<DT>;
     constexpr int LPI = D / 4;
-    const int lane = threadIdx.x & 31, l = lane % LPI;
+    __shared__ __align__(16) uint32_t words[D * 8];
+    __shared__ unsigned char* vblks[8];
+    const int lane = threadIdx.x & 31, l = lane % LPI, grp = threadIdx.x / LPI;
     const unsigned mask = LPI == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
-    const long long item = (static_cast<long long>(blockIdx.x) * SC_STORE_NT + threadIdx.x) / LPI;
-    const int h = static_cast<int>(item % c.kv_heads);
-    const long long bj = item / c.kv_heads;
-    const int j = static_cast<int>(bj % P.ngrp);
-    const long long bl = bj / P.ngrp;
-    if (bl >= P.B) return;
-    const int b = static_cast<int>(bl);
-    if (P.out_lens && h == 0 && j == 0) {
+    const unsigned bj = blockIdx.x / c.kv_heads;
+    const int h = static_cast<int>(blockIdx.x - bj * c.kv_heads);
+    const int b = static_cast<int>(bj / P.tiles), j = static_cast<int>(bj - b * static_cast<unsigned>(P.tiles));
+    if (P.out_lens && h == 0 && j == 0 && grp == 0) {
         const int nl = sc_new_len<LPI>(c, P, b, l, mask);
         if (l == 0) P.out_lens[b] = nl;
     }
     int len, count;
     if (!sc_kept(c, P, b, &len, &count) || count == 0) return;
+    const int tile0 = (len & ~(SC_TILE - 1)) + j * SC_TILE;
+    if (tile0 >= len + count) return;
     const int T = c.block;
-    const int p0 = ((len >> 3) + j) << 3;  // first position of the group
-    if (p0 >= len + count) return;
-    const int t0 = p0 & ~(T - 1);          // and of its block
-    const int from = len > t0 ? len - t0 : 0;                     // tokens of the block written:
-    const int to = len + count - t0 < T ? len + count - t0 : T;  // [from, to)
-    const int id = c.table[static_cast<size_t>(b) * c.max_pages + (t0 >> c.log2_page)];
-    if (id < 0 || id >= c.num_pages) return;
-    unsigned char* blkp = sc_block_ptr<D>(c, id, h, (t0 & (c.page_size - 1)) >> c.log2_block);
-    unsigned char* vblk = blkp + sc_half_bytes<D>(T);
-
+    const int p0 = tile0 + grp * 8;  // first position of the group
+    const int t0 = p0 & ~(T - 1);    // and of its block
     const int g = (p0 - t0) >> 3;
+    uint32_t have = sc_bits8(len - p0, len + count - p0);  // tokens of the group that are written
+    int id = -1;
+    if (have) id = c.table[static_cast<size_t>(b) * c.max_pages + (t0 >> c.log2_page)];
+    if (id < 0 || id >= c.num_pages) have = 0;
+    unsigned char* blkp = sc_block_ptr<D>(c, have ? id : 0, h, (t0 & (c.page_size - 1)) >> c.log2_block);
+    unsigned char* vblk = blkp + sc_half_bytes<D>(T);
     // 8 tokens: 4 dims of each, keys and values
     uint2 raw[16];
-    uint32_t have = 0xffu;
     {
         const typename Ty::T* kp = static_cast<const typename Ty::T*>(P.k) + static_cast<size_t>(h) * D + 4 * l;
         const typename Ty::T* vp = static_cast<const typename Ty::T*>(P.v) + static_cast<size_t>(h) * D + 4 * l;
         const size_t row = static_cast<size_t>(b) * P.n;
-        if (!P.nodes && from <= g * 8 && g * 8 + 8 <= to) {  // a whole group of rows side by side
+        if (!P.nodes && have == 0xffu) {  // a whole group of rows side by side
             const size_t o = (row + (p0 - len)) * static_cast<size_t>(P.stride);
             kp += o;
             vp += o;
@@ -199,13 +219,10 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
                 vp += P.stride;
             }
         } else {
-            have = 0;
             int node[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = g * 8 + i;
-                node[i] = t >= from && t < to ? sc_node(P, b, t0 + t - len) : -1;
-            }
+            for (int i = 0; i < 8; ++i) node[i] = (have >> i) & 1u ? sc_node(P, b, p0 + i - len) : -1;
+            have = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 raw[i] = raw[8 + i] = make_uint2(0u, 0u);
@@ -218,6 +235,8 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
             }
         }
     }
+    const bool all = __syncthreads_and(have == 0xffu);
+    if (have == 0) return;  // (nor is any of its warps needed below)
     // each row's {min, -max}: within the lane, then a reduce-scatter of the
     // 16 rows over the lanes (15 exchanges of one register, and one more at
     // 32 lanes, in place of 5 steps for each row and side)
@@ -280,143 +299,184 @@ __global__ void __launch_bounds__(SC_STORE_NT) sc_append_kernel(CacheView c, App
             vacc[1][e] = m == 0 ? c23 : f2_fma(f2_pack(f, f), c23, vacc[1][e]);
         }
     }
+    uint32_t word[4];  // the lane's dims
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float e0, e1, o0, o1;
+        f2_unpack(vacc[q][0], e0, e1);
+        f2_unpack(vacc[q][1], o0, o1);
+        word[2 * q] = __byte_perm(sc_bits(e0), sc_bits(o0), 0x5410);
+        word[2 * q + 1] = __byte_perm(sc_bits(e1), sc_bits(o1), 0x5410);
+    }
+    if (all) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) words[sc_word(4 * l + q, grp)] = word[q];
+        if (l == 0) vblks[grp] = vblk;
+        __syncthreads();
+        int dim, half;
+        sc_share<D>(T, &dim, &half);
+        const uint4 y = *reinterpret_cast<const uint4*>(words + sc_word(dim, 4 * half));
+        if (T >= 32) {
+            *reinterpret_cast<uint4*>(vblks[4 * half] + dim * (T / 2) + (T == SC_TILE ? 16 * half : 0)) = y;
+        } else {
+            *reinterpret_cast<uint2*>(vblks[4 * half] + dim * (T / 2)) = make_uint2(y.x, y.y);
+            *reinterpret_cast<uint2*>(vblks[4 * half + 2] + dim * (T / 2)) = make_uint2(y.z, y.w);
+        }
+        return;
+    }
     // tokens of the group that are not written keep their codes
     uint32_t keep = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (!((have >> i) & 1u)) keep |= 0xFu << (16 * (i & 1) + 4 * (i >> 1));
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        float e0, e1, o0, o1;
-        f2_unpack(vacc[q][0], e0, e1);
-        f2_unpack(vacc[q][1], o0, o1);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t w = __byte_perm(sc_bits(k ? e1 : e0), sc_bits(k ? o1 : o0), 0x5410);
-            uint32_t* dst = reinterpret_cast<uint32_t*>(vblk + (4 * l + 2 * q + k) * (T / 2) + g * 4);
-            if (keep) w = (w & ~keep) | (*dst & keep);
-            *dst = w;
-        }
+    for (int q = 0; q < 4; ++q) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(vblk + (4 * l + q) * (T / 2) + g * 4);
+        *dst = keep ? (word[q] & ~keep) | (*dst & keep) : word[q];
     }
 }
 
 // The lengths advanced in place, after every block has been written.
-__global__ void __launch_bounds__(SC_STORE_NT) sc_advance_kernel(CacheView c, AppendParams P, int32_t* out_lens) {
+constexpr int SC_ADVANCE_NT = 128;
+__global__ void __launch_bounds__(SC_ADVANCE_NT) sc_advance_kernel(CacheView c, AppendParams P, int32_t* out_lens) {
     pdl_wait_primary();
-    const int b = blockIdx.x * (SC_STORE_NT / 32) + (threadIdx.x >> 5);
+    const int b = blockIdx.x * (SC_ADVANCE_NT / 32) + (threadIdx.x >> 5);
     if (b >= P.B) return;
     const int l = threadIdx.x & 31;
     const int nl = sc_new_len<32>(c, P, b, l, 0xffffffffu);
     if (l == 0) out_lens[b] = nl;
 }
 
+// zero + scale * code of two elements, rounded once.
+template <int DT>
+__device__ __forceinline__ uint32_t sc_value2(uint32_t s, uint32_t code, uint32_t z) {
+    uint32_t d;
+    if constexpr (DT == 0)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(s), "r"(code), "r"(z));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(s), "r"(code), "r"(z));
+    return d;
+}
+// Two codes (bits 0-3 and 16-19 of w) as numbers: below the last bit of 2^7
+// (2^10), which is then taken off.
+template <int DT>
+__device__ __forceinline__ uint32_t sc_numbers2(uint32_t w) {
+    uint32_t d;
+    if constexpr (DT == 0)
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"((w & 0x000F000Fu) | 0x43004300u), "r"(0x43004300u));
+    else
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(0x64006400u));
+    return d;
+}
+
 template <int DT, int D>
-__global__ void __launch_bounds__(SC_STORE_NT) sc_read_kernel(CacheView c, ReadParams P) {
-    using Ty = SC<DT>;
+__global__ void __launch_bounds__(sc_store_threads(D)) sc_read_kernel(CacheView c, ReadParams P) {
+    using T_ = typename SC<DT>::T;
     constexpr int LPI = D / 4;
-    const int l = threadIdx.x % LPI;
-    const long long item = (static_cast<long long>(blockIdx.x) * SC_STORE_NT + threadIdx.x) / LPI;
-    const int h = static_cast<int>(item % c.kv_heads);
-    const long long bj = item / c.kv_heads;
-    const int j = static_cast<int>(bj % P.ngrp);
-    const long long bl = bj / P.ngrp;
-    if (bl >= P.B) return;
-    const int b = static_cast<int>(bl);
+    __shared__ __align__(16) uint32_t words[D * 8];
+    const int l = threadIdx.x % LPI, grp = threadIdx.x / LPI;
+    const unsigned bj = blockIdx.x / c.kv_heads;
+    const int h = static_cast<int>(blockIdx.x - bj * c.kv_heads);
+    const int b = static_cast<int>(bj / P.tiles), j = static_cast<int>(bj - b * static_cast<unsigned>(P.tiles));
     const int len = c.lens[b];
     const long long first = P.first ? P.first[b] : 0;
     const int T = c.block;
-    const long long p0 = ((first >> 3) + j) * 8;  // first position of the group, may be negative
-    if (p0 >= first + P.n) return;
-    const long long t0 = p0 & ~static_cast<long long>(T - 1);  // and of its block
-    const int from = static_cast<int>(first > t0 ? first - t0 : 0);
-    const int to = static_cast<int>(first + P.n - t0 < T ? first + P.n - t0 : T);
-    const unsigned char* blkp = nullptr;
-    bool bad = false;
-    if (t0 >= 0 && t0 < len) {
-        bad = t0 >= sc_capacity(c);
-        if (!bad) {
-            const int id = c.table[static_cast<size_t>(b) * c.max_pages + (t0 >> c.log2_page)];
-            bad = id < 0 || id >= c.num_pages;
-            if (!bad)
-                blkp = sc_block_ptr<D>(c, id, h, (static_cast<int>(t0) & (c.page_size - 1)) >> c.log2_block);
-        }
-    }
-    const unsigned char* vblk = blkp ? blkp + sc_half_bytes<D>(T) : nullptr;
+    const long long tile0 = ((first >> 6) + j) * SC_TILE;  // may be negative
+    if (tile0 >= first + P.n) return;
+    // The block of a position, null where there is none; `bad`: it should be there.
+    auto block = [&](long long pos, bool* bad) -> const unsigned char* {
+        *bad = false;
+        if (pos < 0 || pos >= len) return nullptr;
+        int id = -1;
+        if (pos < sc_capacity(c)) id = c.table[static_cast<size_t>(b) * c.max_pages + (pos >> c.log2_page)];
+        *bad = id < 0 || id >= c.num_pages;
+        return *bad ? nullptr : sc_block_ptr<D>(c, id, h, (static_cast<int>(pos) & (c.page_size - 1)) >> c.log2_block);
+    };
+    const long long p0 = tile0 + grp * 8;  // the group's first position
+    const long long t0 = p0 & ~static_cast<long long>(T - 1);
     const int g = static_cast<int>(p0 - t0) >> 3;
-    // the group's words and parameters; nothing where its block cannot be read
-    uint32_t kw[8], vw[4], kp[8], vp[8];
+    bool bad;
+    const unsigned char* blkp = block(t0, &bad);
+    // the tile's value words, 16 bytes a thread
+    if (P.out_v) {
+        int dim, half;
+        sc_share<D>(T, &dim, &half);
+        bool none;
+        const unsigned char* v0 = T == SC_TILE ? blkp : block(tile0 + 32 * half, &none);
+        uint4 y = make_uint4(0u, 0u, 0u, 0u);
+        if (T >= 32) {
+            if (v0)
+                y = *reinterpret_cast<const uint4*>(v0 + sc_half_bytes<D>(T) + dim * (T / 2) + (T == SC_TILE ? 16 * half : 0));
+        } else {
+            const unsigned char* v1 = block(tile0 + 32 * half + 16, &none);
+            if (v0) {
+                const uint2 x = *reinterpret_cast<const uint2*>(v0 + sc_half_bytes<D>(T) + dim * (T / 2));
+                y.x = x.x, y.y = x.y;
+            }
+            if (v1) {
+                const uint2 x = *reinterpret_cast<const uint2*>(v1 + sc_half_bytes<D>(T) + dim * (T / 2));
+                y.z = x.x, y.w = x.y;
+            }
+        }
+        *reinterpret_cast<uint4*>(words + sc_word(dim, 4 * half)) = y;
+    }
+    // the group's key words and parameters
+    uint32_t kw[8], kp[8], vp[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) kw[i] = kp[i] = vp[i] = 0u;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) vw[q] = 0u;
     if (blkp) {
+        const unsigned char* par = blkp + T * (D / 2) + g * 32;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
-            const uint4 a = *reinterpret_cast<const uint4*>(blkp + T * (D / 2) + (g * 8 + i) * 4);
-            const uint4 e = *reinterpret_cast<const uint4*>(vblk + T * (D / 2) + (g * 8 + i) * 4);
+            const uint4 a = *reinterpret_cast<const uint4*>(par + i * 4);
+            const uint4 e = *reinterpret_cast<const uint4*>(par + sc_half_bytes<D>(T) + i * 4);
             kp[i] = a.x, kp[i + 1] = a.y, kp[i + 2] = a.z, kp[i + 3] = a.w;
             vp[i] = e.x, vp[i + 1] = e.y, vp[i + 2] = e.z, vp[i + 3] = e.w;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             kw[i] = *reinterpret_cast<const uint32_t*>(blkp + (g * 8 + i) * (D / 2) + (l >> 1) * 4);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            vw[q] = *reinterpret_cast<const uint32_t*>(vblk + (4 * l + q) * (T / 2) + g * 4);
     }
+    __syncthreads();
     // rows of the group that are read, and of them those that hold a token
-    uint32_t rows = 0, in = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int t = g * 8 + i;
-        const long long pos = t0 + t;
-        if (t >= from && t < to) rows |= 1u << i;
-        if (pos >= 0 && pos < len) in |= 1u << i;
-    }
-    typename Ty::T* ok = static_cast<typename Ty::T*>(P.out_k);
-    typename Ty::T* ov = static_cast<typename Ty::T*>(P.out_v);
+    const long long before = first - p0, behind = first + P.n - p0, held = p0 < 0 ? 0 : len - p0;
+    const uint32_t rows = sc_bits8(static_cast<int>(before > 0 ? before : 0),  // (above 8 before a tile's later groups)
+                                   static_cast<int>(behind < 8 ? (behind > 0 ? behind : 0) : 8));
+    const uint32_t in = sc_bits8(0, static_cast<int>(held < 8 ? (held > 0 ? held : 0) : 8));
+    if (rows == 0) return;
     const size_t step = static_cast<size_t>(c.kv_heads) * D;
     // (of the group's first row, which may lie before the range)
     const long long o0 = ((static_cast<long long>(b) * P.n + (p0 - first)) * c.kv_heads + h) * D + 4 * l;
-    const uint64_t down = f2_pack(-8388608.f, -8388608.f);
-    const uint32_t sel = 0x7540u + (l & 1);  // a byte of the codes below 2^23's upper bytes
-    uint32_t vlo[4], vhi[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        vlo[q] = vw[q] & 0x0F0F0F0Fu;
-        vhi[q] = (vw[q] >> 4) & 0x0F0F0F0Fu;
-    }
-    auto value = [&](uint32_t a, uint32_t e, uint64_t s2, uint64_t z2) {  // two codes as floats above 2^23
-        float x, y;
-        f2_unpack(f2_fma(s2, f2_add(f2_pack(__uint_as_float(a), __uint_as_float(e)), down), z2), x, y);
-        return Ty::pack(x, y);
-    };
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (!((rows >> i) & 1u)) continue;
-        const bool token = (in >> i) & 1u;
-        const size_t o = static_cast<size_t>(o0 + static_cast<long long>(i) * static_cast<long long>(step));
-        const uint32_t fill = token && bad ? 0x7fff7fffu : 0u;
-        if (ok) {
-            const float s = Ty::lo(kp[i]), z = Ty::hi(kp[i]);
-            const uint64_t s2 = f2_pack(s, s), z2 = f2_pack(z, z);
-            const uint32_t lo = kw[i] & 0x0F0F0F0Fu, hi = (kw[i] >> 4) & 0x0F0F0F0Fu;
-            uint2 y = make_uint2(value(__byte_perm(lo, 0x4B000000u, sel), __byte_perm(lo, 0x4B000000u, sel + 2), s2, z2),
-                                 value(__byte_perm(hi, 0x4B000000u, sel), __byte_perm(hi, 0x4B000000u, sel + 2), s2, z2));
-            if (!token || bad) y = make_uint2(fill, fill);
-            *reinterpret_cast<uint2*>(ok + o) = y;
+    auto put = [&](T_* out, int i, uint32_t par, uint32_t c01, uint32_t c23) {  // codes as numbers
+        const uint32_t s2 = __byte_perm(par, 0u, 0x1010), z2 = __byte_perm(par, 0u, 0x3232);
+        uint2 y = make_uint2(sc_value2<DT>(s2, c01, z2), sc_value2<DT>(s2, c23, z2));
+        if ((rows & in) != 0xffu || bad) {
+            if (!((rows >> i) & 1u)) return;
+            if (!((in >> i) & 1u)) y = make_uint2(0u, 0u);
+            else if (bad) y = make_uint2(0x7fff7fffu, 0x7fff7fffu);
         }
-        if (ov) {
-            const float s = Ty::lo(vp[i]), z = Ty::hi(vp[i]);
-            const uint64_t s2 = f2_pack(s, s), z2 = f2_pack(z, z);
-            // token i: nibble (i / 2) of the half i % 2, so byte i / 4 + 2 (i % 2), its upper half for i / 2 odd
-            const uint32_t vs = 0x7540u + (i >> 2) + 2 * (i & 1);
-            uint32_t x[4];
+        *reinterpret_cast<uint2*>(out + o0 + static_cast<long long>(i) * static_cast<long long>(step)) = y;
+    };
+    if (P.out_k) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = __byte_perm(((i >> 1) & 1) ? vhi[q] : vlo[q], 0x4B000000u, vs);
-            uint2 y = make_uint2(value(x[0], x[1], s2, z2), value(x[2], x[3], s2, z2));
-            if (!token || bad) y = make_uint2(fill, fill);
-            *reinterpret_cast<uint2*>(ov + o) = y;
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = kw[i] >> (8 * (l & 1));
+            put(static_cast<T_*>(P.out_k), i, kp[i], sc_numbers2<DT>(w), sc_numbers2<DT>(w >> 4));
+        }
+    }
+    if (P.out_v) {
+        uint32_t vw[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) vw[q] = words[sc_word(4 * l + q, grp)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x[4];  // tokens 2 i, 2 i + 1 of the lane's dims
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = sc_numbers2<DT>(vw[q] >> (4 * i));
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                put(static_cast<T_*>(P.out_v), 2 * i + e, vp[2 * i + e], __byte_perm(x[0], x[1], e ? 0x7632 : 0x5410),
+                    __byte_perm(x[2], x[3], e ? 0x7632 : 0x5410));
         }
     }
 }

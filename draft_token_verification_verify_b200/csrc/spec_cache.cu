@@ -275,25 +275,24 @@ sv_status_t spec_cache_append(const sv_cache_t* cache, const void* k, const void
     P.nodes = nodes;
     P.nodes_stride = nodes_stride;
     P.out_lens = in_place ? nullptr : out_lens;
-    P.ngrp = static_cast<int>((static_cast<long long>(n) + 6) / 8 + 1);
-    const long long items = static_cast<long long>(B) * P.ngrp * c.kv_heads;
-    const long long blocks = ceil_div(items, sv::SC_STORE_NT / (D / 4));
-    if (blocks > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+    P.tiles = static_cast<int>((static_cast<long long>(n) + sv::SC_TILE - 2) / sv::SC_TILE + 1);
+    if (n > (1 << 30) || static_cast<double>(B) * P.tiles * c.kv_heads > 2147483647.0) return SV_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void (*fn)(sv::CacheView, sv::AppendParams) =
         D == 64 ? (dt ? sv::sc_append_kernel<1, 64> : sv::sc_append_kernel<0, 64>)
                 : (dt ? sv::sc_append_kernel<1, 128> : sv::sc_append_kernel<0, 128>);
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(sv::SC_STORE_NT, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(B) * P.tiles * c.kv_heads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(sv::sc_store_threads(D)), 1, 1);
     cfg.stream = st;
     sv_status_t r = launched(cudaLaunchKernelEx(&cfg, fn, c, P));
     if (r != SV_OK || !in_place) return r;
     cudaLaunchAttribute a[1];
     a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     a[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(B, sv::SC_STORE_NT / 32)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(B, sv::SC_ADVANCE_NT / 32)), 1, 1);
+    cfg.blockDim = dim3(sv::SC_ADVANCE_NT, 1, 1);
     cfg.attrs = a;
     cfg.numAttrs = 1;
     return launched(cudaLaunchKernelEx(&cfg, sv::sc_advance_kernel, c, P, out_lens));
@@ -317,16 +316,14 @@ sv_status_t spec_cache_read(const sv_cache_t* cache, int B, int n, const int32_t
     P.out_v = out_v;
     P.B = B;
     P.n = n;
-    P.ngrp = static_cast<int>((static_cast<long long>(n) + 6) / 8 + 1);
-    const long long items = static_cast<long long>(B) * P.ngrp * c.kv_heads;
-    const long long blocks = ceil_div(items, sv::SC_STORE_NT / (D / 4));
-    if (blocks > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+    P.tiles = static_cast<int>((static_cast<long long>(n) + sv::SC_TILE - 2) / sv::SC_TILE + 1);
+    if (static_cast<double>(B) * P.tiles * c.kv_heads > 2147483647.0) return SV_ERR_UNSUPPORTED;
     void (*fn)(sv::CacheView, sv::ReadParams) = D == 64 ? (dt ? sv::sc_read_kernel<1, 64> : sv::sc_read_kernel<0, 64>)
                                                         : (dt ? sv::sc_read_kernel<1, 128> : sv::sc_read_kernel<0, 128>);
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(sv::SC_STORE_NT, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(B) * P.tiles * c.kv_heads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(sv::sc_store_threads(D)), 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     return launched(cudaLaunchKernelEx(&cfg, fn, c, P));
 }
