@@ -10,6 +10,8 @@
 // twice.
 #pragma once
 
+#include <type_traits>
+
 #include "sc_common.cuh"
 
 namespace sv {
@@ -447,38 +449,47 @@ __global__ void __launch_bounds__(sc_store_threads(D)) sc_read_kernel(CacheView 
     const size_t step = static_cast<size_t>(c.kv_heads) * D;
     // (of the group's first row, which may lie before the range)
     const long long o0 = ((static_cast<long long>(b) * P.n + (p0 - first)) * c.kv_heads + h) * D + 4 * l;
-    auto put = [&](T_* out, int i, uint32_t par, uint32_t c01, uint32_t c23) {  // codes as numbers
-        const uint32_t s2 = __byte_perm(par, 0u, 0x1010), z2 = __byte_perm(par, 0u, 0x3232);
-        uint2 y = make_uint2(sc_value2<DT>(s2, c01, z2), sc_value2<DT>(s2, c23, z2));
-        if ((rows & in) != 0xffu || bad) {
-            if (!((rows >> i) & 1u)) return;
-            if (!((in >> i) & 1u)) y = make_uint2(0u, 0u);
-            else if (bad) y = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+    uint32_t vw[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) vw[q] = words[sc_word(4 * l + q, grp)];
+    auto write = [&](auto whole) {  // 8 rows that all hold tokens, or any
+        auto put = [&](T_* out, int i, uint32_t par, uint32_t c01, uint32_t c23) {  // codes as numbers
+            const uint32_t s2 = __byte_perm(par, 0u, 0x1010), z2 = __byte_perm(par, 0u, 0x3232);
+            uint2 y = make_uint2(sc_value2<DT>(s2, c01, z2), sc_value2<DT>(s2, c23, z2));
+            if constexpr (!decltype(whole)::value) {
+                if (!((rows >> i) & 1u)) return;
+                if (!((in >> i) & 1u)) y = make_uint2(0u, 0u);
+                else if (bad) y = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+            }
+            *reinterpret_cast<uint2*>(out) = y;
+        };
+        if (P.out_k) {
+            T_* out = static_cast<T_*>(P.out_k) + o0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w = kw[i] >> (8 * (l & 1));
+                put(out, i, kp[i], sc_numbers2<DT>(w), sc_numbers2<DT>(w >> 4));
+                out += step;
+            }
         }
-        *reinterpret_cast<uint2*>(out + o0 + static_cast<long long>(i) * static_cast<long long>(step)) = y;
+        if (P.out_v) {
+            T_* out = static_cast<T_*>(P.out_v) + o0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x[4];  // tokens 2 i, 2 i + 1 of the lane's dims
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = sc_numbers2<DT>(vw[q] >> (4 * i));
+                put(out, 2 * i, vp[2 * i], __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
+                out += step;
+                put(out, 2 * i + 1, vp[2 * i + 1], __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+                out += step;
+            }
+        }
     };
-    if (P.out_k) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w = kw[i] >> (8 * (l & 1));
-            put(static_cast<T_*>(P.out_k), i, kp[i], sc_numbers2<DT>(w), sc_numbers2<DT>(w >> 4));
-        }
-    }
-    if (P.out_v) {
-        uint32_t vw[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) vw[q] = words[sc_word(4 * l + q, grp)];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t x[4];  // tokens 2 i, 2 i + 1 of the lane's dims
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = sc_numbers2<DT>(vw[q] >> (4 * i));
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                put(static_cast<T_*>(P.out_v), 2 * i + e, vp[2 * i + e], __byte_perm(x[0], x[1], e ? 0x7632 : 0x5410),
-                    __byte_perm(x[2], x[3], e ? 0x7632 : 0x5410));
-        }
-    }
+    if ((rows & in) == 0xffu && !bad)
+        write(std::true_type{});
+    else
+        write(std::false_type{});
 }
 
 }  // namespace sv
