@@ -39,7 +39,16 @@ struct ReadParams {
     int tiles;
 };
 
-// min of bf16 / fp16 pairs, NaN if either is.
+// max and min of bf16 / fp16 pairs, NaN if either is.
+template <int DT>
+__device__ __forceinline__ uint32_t sc_max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (DT == 0)
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 template <int DT>
 __device__ __forceinline__ uint32_t sc_min2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -118,9 +127,9 @@ __device__ __noinline__ float sc_divided(float d, float scale) {
     const float x = scale > 0.f ? fminf(rintf(__fdiv_rn(d, scale)), 15.f) : 0.f;
     return x >= 0.f ? x : 0.f;
 }
-__device__ __forceinline__ void sc_codes4(uint64_t x01, uint64_t x23, float zero, float scale, float inv,
+__device__ __forceinline__ void sc_codes4(uint64_t x01, uint64_t x23, uint64_t nz, uint64_t i2, const float& scale,
                                           uint64_t& c01, uint64_t& c23) {
-    const uint64_t nz = f2_pack(-zero, -zero), i2 = f2_pack(inv, inv), minus = f2_pack(-1.f, -1.f);
+    const uint64_t minus = f2_pack(-1.f, -1.f);
     const uint64_t up = f2_pack(12582912.f, 12582912.f), down = f2_pack(-12582912.f, -12582912.f);
     const uint64_t d01 = f2_add(x01, nz), d23 = f2_add(x23, nz);
     const uint64_t q01 = f2_mul(d01, i2), q23 = f2_mul(d23, i2);
@@ -130,20 +139,22 @@ __device__ __forceinline__ void sc_codes4(uint64_t x01, uint64_t x23, float zero
     f2_unpack(f2_fma(c01, minus, q01), e0, e1);
     f2_unpack(f2_fma(c23, minus, q23), e2, e3);
     const float off = fmaxf(fmaxf(fabsf(e0), fabsf(e1)), fmaxf(fabsf(e2), fabsf(e3)));
-    if (off >= 0.49998f || inv != inv) {
-        float c[4], d[4];
+    if (!(off < 0.49998f)) {  // also NaN
+        const float s = scale;
+        float c[4], d[4], inv, inv_;
+        f2_unpack(i2, inv, inv_);
         f2_unpack(c01, c[0], c[1]);
         f2_unpack(c23, c[2], c[3]);
         f2_unpack(d01, d[0], d[1]);
         f2_unpack(d23, d[2], d[3]);
         if (inv == inv) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc_near(c[i], d[i], scale, 0.5f * scale);
+            for (int i = 0; i < 4; ++i) sc_near(c[i], d[i], s, 0.5f * s);
             c01 = f2_add(f2_add(f2_pack(c[0], c[1]), up), down);
             c23 = f2_add(f2_add(f2_pack(c[2], c[3]), up), down);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c[i] = sc_divided(d[i], scale);
+            for (int i = 0; i < 4; ++i) c[i] = sc_divided(d[i], s);
             c01 = f2_pack(c[0], c[1]);
             c23 = f2_pack(c[2], c[3]);
         }
@@ -180,6 +191,8 @@ __global__ void __launch_bounds__(sc_store_threads(D)) sc_append_kernel(CacheVie
     constexpr int LPI = D / 4;
     __shared__ __align__(16) uint32_t words[D * 8];
     __shared__ unsigned char* vblks[8];
+    __shared__ ulonglong2 pars[8][16];  // a row's -zero and 1 / scale, twice each
+    __shared__ float scales[8][16];
     const int lane = threadIdx.x & 31, l = lane % LPI, grp = threadIdx.x / LPI;
     const unsigned mask = LPI == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
     const unsigned bj = blockIdx.x / c.kv_heads;
@@ -246,7 +259,7 @@ __global__ void __launch_bounds__(sc_store_threads(D)) sc_append_kernel(CacheVie
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const uint32_t lo = sc_min2<DT>(raw[i].x, raw[i].y);
-        const uint32_t hi = sc_min2<DT>(raw[i].x ^ 0x80008000u, raw[i].y ^ 0x80008000u);
+        const uint32_t hi = sc_max2<DT>(raw[i].x, raw[i].y) ^ 0x80008000u;
         x[i] = sc_min2<DT>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
     }
     sc_fold<DT, 16, 1>(x, l, mask);
@@ -254,33 +267,30 @@ __global__ void __launch_bounds__(sc_store_threads(D)) sc_append_kernel(CacheVie
     sc_fold<DT, 4, 4>(x, l, mask);
     sc_fold<DT, 2, 8>(x, l, mask);
     if (LPI == 32) x[0] = sc_min2<DT>(x[0], __shfl_xor_sync(mask, x[0], 16));
-    // lane l holds row 8 b0 + 4 b1 + 2 b2 + b3 (b the bits of l): its (scale, zero), and what a
-    // difference from zero is multiplied by (NaN: it is divided, see sc_codes4)
-    uint32_t par;
-    float inv;
-    {
+    // lane l holds row 8 b0 + 4 b1 + 2 b2 + b3 (b the bits of l): it leaves its (scale, zero) in the block, and
+    // for the group what a difference from zero is multiplied by (NaN: it is divided, see sc_codes4)
+    if (l < 16) {
         const float mn = Ty::lo(x[0]), mx = -Ty::hi(x[0]);
         const float sc = Ty::round(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
         const bool fine = fabsf(mn) < __builtin_huge_valf() && fabsf(mx) < __builtin_huge_valf() &&
                           fabsf(sc) < __builtin_huge_valf();
-        par = fine ? Ty::pack(sc, mn) : 0x00007fffu;  // a NaN in either type
-        inv = fine && sc >= (DT == 0 ? 1e-30f : 6.2e-5f) ? __fdividef(1.f, sc) : __int_as_float(0x7fffffff);
-    }
-    if (l < 16) {
+        const float inv = fine && sc >= (DT == 0 ? 1e-30f : 6.2e-5f) ? __fdividef(1.f, sc) : __int_as_float(0x7fffffff);
         const int i = 8 * (l & 1) + 4 * ((l >> 1) & 1) + 2 * ((l >> 2) & 1) + ((l >> 3) & 1);  // the lane's row
+        pars[grp][i] = make_ulonglong2(f2_pack(-mn, -mn), f2_pack(inv, inv));
+        scales[grp][i] = fine ? sc : 0.f;
         if ((have >> (i & 7)) & 1u)
-            *reinterpret_cast<uint32_t*>((i < 8 ? blkp : vblk) + T * (D / 2) + (g * 8 + (i & 7)) * 4) = par;
+            *reinterpret_cast<uint32_t*>((i < 8 ? blkp : vblk) + T * (D / 2) + (g * 8 + (i & 7)) * 4) =
+                fine ? Ty::pack(sc, mn) : 0x00007fffu;  // a NaN in either type
     }
+    __syncwarp(mask);
     uint32_t before = 0;
     uint64_t vacc[2][2];  // dims {0, 1} and {2, 3} of the lane: the even and the odd tokens' codes
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const int src = ((i >> 3) & 1) | ((i >> 1) & 2) | ((i << 1) & 4) | ((i << 3) & 8);
-        const uint32_t p = __shfl_sync(mask, par, src, LPI);
-        const float iv = __shfl_sync(mask, inv, src, LPI);
+        const ulonglong2 y = pars[grp][i];
         uint64_t c01, c23;
-        sc_codes4(f2_pack(Ty::lo(raw[i].x), Ty::hi(raw[i].x)), f2_pack(Ty::lo(raw[i].y), Ty::hi(raw[i].y)), Ty::hi(p),
-                  Ty::lo(p), iv, c01, c23);
+        sc_codes4(f2_pack(Ty::lo(raw[i].x), Ty::hi(raw[i].x)), f2_pack(Ty::lo(raw[i].y), Ty::hi(raw[i].y)), y.x, y.y,
+                  scales[grp][i], c01, c23);
         if (i < 8) {
             // a key row's word w: dims 8w.. from lanes 2w (low byte of each half) and 2w+1
             float lo, hi;
