@@ -537,7 +537,6 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                         if constexpr (DT == 1) pl[t >> 1][2 * (t & 1) + e] = SC<0>::pack(s0 - SC<0>::lo(hi), s1 - SC<0>::hi(hi));
                     }
                 }
-                __syncwarp();
 #pragma unroll
                 for (int u4 = 0; u4 < NV; u4 += 4) {
                     uint2 vw[4];

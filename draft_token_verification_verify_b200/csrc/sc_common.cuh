@@ -147,10 +147,11 @@ __device__ __forceinline__ bool sc_wait(uint64_t* bar, uint32_t parity, uint64_t
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
-    for (;;) {
+    for (uint32_t it = 1; it < 0x80000000u; ++it) {  // (whatever the timer says)
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) return false;
     }
+    return false;
 }
 
 // fp32 pairs
