@@ -9,8 +9,9 @@
 // so that a weight's rounding meets code - 8.
 //
 // K_attend: a warp takes 16 rows (m16n8k16 MMAs) and tiles of 64 tokens, with a
-// ring of bulk copies of its own; there is no barrier between the warps until
-// the (maximum, sum, output) of a segment's four are merged.  The fragment order
+// ring of bulk copies of its own, and nothing makes it wait for another: a
+// barrier at each segment's end, where four warps of a CTA took its tiles in
+// turn, cost a third of the time at 24 tiles a segment.  The fragment order
 // is chosen so that a lane's operands are contiguous in the block: 16 (8) bytes
 // of a key row hold the lane's share of the whole dot product, 8 bytes of a
 // value row its 16 tokens.  The reference maximum of a row is not moved until a
@@ -18,9 +19,9 @@
 //
 // The work: a segment is (sequence, head, block of 16 rows) and has
 // ceil(len / 64) tiles of the cache and ceil(n / 64) units of scored
-// positions.  CTAs come in groups, one for each of up to SC_LANES row blocks;
+// positions.  Warps come in groups, one for each of up to SC_LANES row blocks;
 // the segments' units in a row are cut into equal ranges, one for each group of
-// a single wave, so that a group's CTAs walk the same tiles side by side and
+// a single wave, so that a group's warps walk the same tiles side by side and
 // all but the first find them in L2.  A segment that is cut leaves partial sums
 // that K_join adds in the order of the parts.
 #pragma once
@@ -51,16 +52,15 @@ struct AttendParams {
     long long q_stride, kv_stride;  // elements between tokens
     int B, n, q_heads, group;
     int rows;           // n * group
-    int lanes, passes;  // row blocks of a group of CTAs, and times it walks a head: block pass * lanes + lane
-    int cut;            // groups of CTAs that share the units
-    int whole;  // a CTA takes one whole segment: nothing is cut, and there is no K_join (and no status)
+    int lanes, passes;  // row blocks of a group of warps, and times it walks a head: block pass * lanes + lane
+    int cut;            // groups of warps that share the units
     float scale;
     void* out;
     float* out_lse;
     // workspace
-    float* part_o;   // [grid][2][rows of a block][D]
-    float2* part_ml; // [grid][2][rows of a block]
-    int4* desc;      // [grid]: {segment cut here that begins in this CTA: b, head * passes + pass, parts, error}
+    float* part_o;   // [warps][2][rows of a block][D]
+    float2* part_ml; // [warps][2][rows of a block]
+    int4* desc;      // [warps]: {segment cut here that begins in this warp: b, head * passes + pass, parts, error}
     unsigned long long timeout_ns;
     int test_hook;
     int32_t* out_status;
@@ -81,28 +81,22 @@ __device__ __forceinline__ int sc_units(const AttendParams& P, int b) {
     return u > 0 ? u : 1;
 }
 
-// A group's range of the segments' units, found by all its threads.
+// A range of the segments' units, and where it begins.
 struct Range {
-    long long total, chunk, g0, g1;  // units in all; of a group; this group's
+    long long total, chunk, g0, g1;  // units in all; of a range; this one
     int b;                           // sequence that holds g0
     long long before;                // units before that sequence
 };
 
-template <int NT>
-__device__ __forceinline__ Range sc_range(const AttendParams& P, int index) {
-    __shared__ long long scan[NT / 32];
-    __shared__ long long found[2];
+// Warp w of CTA i is number i + w * CTAs: few ranges spread over all SMs.
+__device__ __forceinline__ int sc_warp_number(int w) { return static_cast<int>(blockIdx.x + w * gridDim.x); }
+
+// The range of each of a CTA's warps, found by all its threads.
+__device__ __forceinline__ Range sc_range(const AttendParams& P) {
+    __shared__ long long scan[SC_WARPS];
+    __shared__ long long found[SC_WARPS][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (P.whole) {  // (not a range of units: the segment's number)
-        const int segs = P.c.kv_heads * P.passes;
-        Range r;
-        r.b = index / segs;
-        r.g0 = index - r.b * segs;
-        r.g1 = r.g0 + 1;
-        r.total = r.chunk = r.before = 0;
-        return r;
-    }
-    const int per = (P.B + NT - 1) / NT;
+    const int per = (P.B + SC_NT - 1) / SC_NT;
     const long long segs = static_cast<long long>(P.c.kv_heads) * P.passes;
     long long mine = 0;
 #pragma unroll 1
@@ -117,7 +111,7 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int index) {
     __syncthreads();
     long long base = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
+    for (int w = 0; w < SC_WARPS; ++w) {
         if (w < warp) base += scan[w];
         total += scan[w];
     }
@@ -126,28 +120,38 @@ __device__ __forceinline__ Range sc_range(const AttendParams& P, int index) {
     // (rounded up, or one more: a double's error never makes the ranges too short)
     r.chunk = static_cast<long long>(static_cast<double>(r.total) / P.cut) + 1;
     if (r.chunk < SC_MIN_TILES) r.chunk = SC_MIN_TILES;
-    r.g0 = r.chunk * index;
-    r.g1 = r.g0 + r.chunk < r.total ? r.g0 + r.chunk : r.total;
-    long long at = (base + incl - mine) * segs;
-    if (r.g0 < r.g1 && r.g0 >= at && r.g0 < at + mine * segs) {
-        int b = tid * per;
 #pragma unroll 1
-        for (;; ++b) {
-            const long long u = sc_units(P, b) * segs;
-            if (r.g0 < at + u) break;
-            at += u;
+    for (int w = 0; w < SC_WARPS; ++w) {
+        const long long g0 = r.chunk * (sc_warp_number(w) / P.lanes);
+        long long at = (base + incl - mine) * segs;
+        if (g0 >= at && g0 < at + mine * segs) {
+            int b = tid * per;
+#pragma unroll 1
+            for (;; ++b) {
+                const long long u = sc_units(P, b) * segs;
+                if (g0 < at + u) break;
+                at += u;
+            }
+            found[w][0] = b;
+            found[w][1] = at;
         }
-        found[0] = b;
-        found[1] = at;
     }
     __syncthreads();
-    r.b = static_cast<int>(found[0]);
-    r.before = found[1];
-    __syncthreads();
+    const int index = sc_warp_number(warp) / P.lanes;
+    r.g0 = r.chunk * index;
+    r.g1 = r.g0 + r.chunk < r.total ? r.g0 + r.chunk : r.total;
+    if (index >= P.cut || r.g0 >= r.g1) {
+        r.g0 = r.g1 = 0;
+        r.b = 0;
+        r.before = 0;
+        return r;
+    }
+    r.b = static_cast<int>(found[warp][0]);
+    r.before = found[warp][1];
     return r;
 }
 
-// A walk over the parts of segments in a CTA's range.
+// A walk over the parts of segments in a range.
 struct Walk {
     int b, hr;       // sequence; head * passes + pass
     int units, len;  // of the sequence
@@ -167,18 +171,21 @@ struct Walk {
     __device__ __forceinline__ void begin(const AttendParams& P, const Range& r) {
         b = __shfl_sync(0xffffffffu, r.b, 0);
         sequence(P);
-        if (P.whole) {
-            hr = __shfl_sync(0xffffffffu, static_cast<int>(r.g0), 0);
-            u0 = left = 0;
-            u1 = units;
-            return;
-        }
         const long long in = r.g0 - r.before;
         hr = __shfl_sync(0xffffffffu, static_cast<int>(static_cast<double>(in) / units), 0);  // exact below 2^53
         u0 = __shfl_sync(0xffffffffu, static_cast<int>(in - static_cast<long long>(hr) * units), 0);
         left = __shfl_sync(0xffffffffu, static_cast<int>(r.g1 - r.g0), 0);
         u1 = units - u0 < left ? units : u0 + left;
         left -= u1 - u0;
+    }
+    // One segment and nothing else.
+    __device__ __forceinline__ void segment(const AttendParams& P, int number) {
+        const int segs = P.c.kv_heads * P.passes;
+        b = number / segs;
+        hr = number - b * segs;
+        sequence(P);
+        u0 = left = 0;
+        u1 = units;
     }
     // The next segment; false behind the range.
     __device__ __forceinline__ bool next(const AttendParams& P) {
@@ -195,7 +202,7 @@ struct Walk {
     }
     // Whether this part is the whole segment.
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
-    // Groups that hold parts of a segment begun here and cut by the range's end.
+    // Ranges that hold parts of a segment begun here and cut by the range's end.
     __device__ __forceinline__ int parts(int chunk) const { return 1 + (units - u1 + chunk - 1) / chunk; }
 };
 
@@ -205,38 +212,43 @@ __device__ __forceinline__ size_t sc_out_row(const AttendParams& P, int b, int h
     return (static_cast<size_t>(b) * P.n + node) * P.q_heads + head * P.group + g;
 }
 
-template <int D>
+template <int D, bool WHOLE>
 struct AttendSmem {
     static constexpr int STAGES = 2;  // tiles in flight for each warp
     // Blocks of a tile lie `bstride` bytes apart: shorter blocks are padded so
     // that the four quarter-tiles of a value read fall into different banks.
     static constexpr int TILE = 2 * sc_half_bytes<D>(SC_BLOCK) + 128;
     static constexpr int RING = SC_WARPS * STAGES * TILE;
-    static constexpr int MERGE_ROW = D + 4;  // floats
-    static constexpr int MERGE = SC_ROWS * MERGE_ROW * 4;  // a warp's output, or its staged value rows
+    static constexpr int STAGE_ROW = D + 8;  // elements: a warp's staged value rows, or output rows
+    static constexpr int MERGE_ROW = D + 4;  // floats: its output, to be merged with the other warps'
+    static constexpr int MERGE = SC_ROWS * (WHOLE ? MERGE_ROW * 4 : STAGE_ROW * 2);
     static constexpr int OFF_ML = RING + SC_WARPS * MERGE;
     static constexpr int OFF_PAR = OFF_ML + SC_WARPS * SC_ROWS * 8;  // float [warps][32 token pairs][8]
     static constexpr int OFF_BAR = OFF_PAR + SC_WARPS * 1024;
     static constexpr int BYTES = OFF_BAR + SC_WARPS * STAGES * 8;
-    static_assert(SC_ROWS * (D + 8) * 2 <= MERGE, "staged value rows fit the merge buffer");
+    static_assert(SC_ROWS * STAGE_ROW * 2 <= MERGE, "staged rows fit the merge buffer");
     static_assert(OFF_BAR % 8 == 0 && sc_ctas(D) * (BYTES + 1024) <= 228 * 1024, "an SM's shared memory");
 };
 
-template <int DT, int D>
+// WHOLE: a CTA takes one segment, its warps tiles in turn, and there is no
+// K_join (and no status).  Otherwise a warp takes a range of units by itself.
+template <int DT, int D, bool WHOLE>
 __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __grid_constant__ AttendParams P) {
     using Ty = SC<DT>;
-    using Sm = AttendSmem<D>;
+    using Sm = AttendSmem<D, WHOLE>;
     using T = typename Ty::T;
     constexpr unsigned ALL = 0xffffffffu;
     constexpr int STAGES = Sm::STAGES;
     constexpr int KS = D / 16;   // k-steps of a dot product
     constexpr int KW = D / 32;   // 32-bit words of a lane's share of a key row
     constexpr int NV = D / 8;    // n-tiles of the output
+    constexpr int STEP = WHOLE ? SC_WARPS : 1;  // units to a warp's next one
     extern __shared__ __align__(128) unsigned char sc_raw[];
     // (the broadcast tells the compiler that a warp works as one)
     const int tid = threadIdx.x, warp = __shfl_sync(ALL, tid >> 5, 0), lane = tid & 31;
     const int r8 = lane >> 2, q4 = lane & 3;
-    const int index = blockIdx.x / P.lanes, row_lane = blockIdx.x - index * P.lanes;  // group, and place in it
+    const int number = WHOLE ? blockIdx.x : sc_warp_number(warp);
+    const int index = number / P.lanes, row_lane = number - index * P.lanes;  // group, and place in it
     unsigned char* ring = sc_raw + warp * STAGES * Sm::TILE;
     float* merge = reinterpret_cast<float*>(sc_raw + Sm::RING + warp * Sm::MERGE);
     float2* ml = reinterpret_cast<float2*>(sc_raw + Sm::OFF_ML);
@@ -246,10 +258,20 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
     const float nan = __int_as_float(0x7fffffff);
 
     pdl_launch_dependents();
-    const Range R = sc_range<SC_NT>(P, index);
     bool error = false;
-    if (tid == 0 && !P.whole) P.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (R.g0 >= R.g1) return;
+    Range R;
+    if constexpr (!WHOLE) {
+        R = sc_range(P);
+        if (lane == 0 && index < P.cut) P.desc[number] = make_int4(-1, 0, 0, 0);
+        if (R.g0 >= R.g1) return;
+    }
+    auto begin = [&](Walk& walk) {
+        if constexpr (WHOLE)
+            walk.segment(P, index);
+        else
+            walk.begin(P, R);
+    };
+    const int u_first = WHOLE ? warp : 0;
     if (lane == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
@@ -265,8 +287,8 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
     const size_t block_bytes = 2 * sc_half_bytes<D>(c.block);
     const size_t head_bytes = block_bytes * (c.page_size >> c.log2_block), page_bytes = head_bytes * c.kv_heads;
     Walk iw;
-    iw.begin(P, R);
-    iw.u = iw.u0 + warp;
+    begin(iw);
+    iw.u = iw.u0 + u_first;
     bool more = true;
     int iw_end = 0;  // behind the part's cache tiles
     int ahead_id = 0, issued = 0, used = 0;
@@ -285,7 +307,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
 #pragma unroll 1
         while (iw.u >= iw_end) {
             if (!(more = iw.next(P))) return;
-            iw.u = iw.u0 + warp;
+            iw.u = iw.u0 + u_first;
             part();
         }
         const int t = iw.u * SC_BLOCK + (lane << c.log2_block);
@@ -322,7 +344,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
         }
         __syncwarp();
         ++issued;
-        iw.u += SC_WARPS;
+        iw.u += STEP;
         fetch();
     };
     fetch();
@@ -343,7 +365,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
     const uint32_t half_bytes = sc_half_bytes<D>(Tb), v_step = 8 * (Tb / 2);
 
     Walk w;
-    w.begin(P, R);
+    begin(w);
 #pragma unroll 1
     for (bool go = true; go; go = w.next(P)) {
         const int head = w.hr / P.passes, row0 = ((w.hr - head * P.passes) * P.lanes + row_lane) * SC_ROWS;
@@ -424,7 +446,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
         };
 
 #pragma unroll 1
-        for (int u = w.u0 + warp; u < w.u1; u += SC_WARPS) {
+        for (int u = w.u0 + u_first; u < w.u1; u += STEP) {
             if (u * SC_BLOCK < w.len) {
                 // ---- a tile of 64 cached tokens ----
                 const int s = used % STAGES;
@@ -722,84 +744,118 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
             }
         }
 
-        // ---- merge the warps: 16 rows of (reference, sum, output) each ----
         const float os = DT == 0 ? SC_2P69 : 1.f;
+        float ls[2], zs[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float a, b;
             f2_unpack(l[e], a, b);
-            float ls = a + b;
+            ls[e] = a + b;
             f2_unpack(z[e], a, b);
-            float zs = a + b;
-            ls += __shfl_xor_sync(ALL, ls, 1);
-            ls += __shfl_xor_sync(ALL, ls, 2);
-            zs += __shfl_xor_sync(ALL, zs, 1);
-            zs += __shfl_xor_sync(ALL, zs, 2);
-            const int r = r8 + 8 * e;
-            if (q4 == 0) ml[warp * SC_ROWS + r] = make_float2(m[e], ls);
-#pragma unroll
-            for (int u = 0; u < NV; ++u)
-                *reinterpret_cast<float2*>(merge + r * Sm::MERGE_ROW + u * 8 + 2 * q4) =
-                    make_float2(fmaf(o[u][2 * e] - o8[2 * e], os, zs), fmaf(o[u][2 * e + 1] - o8[2 * e], os, zs));
+            zs[e] = a + b;
+            ls[e] += __shfl_xor_sync(ALL, ls[e], 1);
+            ls[e] += __shfl_xor_sync(ALL, ls[e], 2);
+            zs[e] += __shfl_xor_sync(ALL, zs[e], 1);
+            zs[e] += __shfl_xor_sync(ALL, zs[e], 2);
         }
-        __syncthreads();
-        const bool whole = w.whole();
-        const int slot = blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0);
-        const float* all = reinterpret_cast<const float*>(sc_raw + Sm::RING);
-        constexpr int PER = SC_NT / SC_ROWS;  // threads of a row
-        const int r = tid / PER, cpart = tid % PER;
-        float M = SC_NEG_INF, L = 0.f, wt[SC_WARPS];
+        auto value = [&](int e, int u) {  // dims 8 u + 2 q4, + 1 of the row r8 + 8 e, not yet divided by the sum
+            return make_float2(fmaf(o[u][2 * e] - o8[2 * e], os, zs[e]), fmaf(o[u][2 * e + 1] - o8[2 * e], os, zs[e]));
+        };
+        if constexpr (!WHOLE) {
+            if (w.whole()) {  // through shared memory, to write rows
+                T* stage = reinterpret_cast<T*>(merge);
+                __syncwarp();
 #pragma unroll
-        for (int i = 0; i < SC_WARPS; ++i) M = fmaxf(M, ml[i * SC_ROWS + r].x);
+                for (int e = 0; e < 2; ++e) {
+                    const float norm = ls[e] != ls[e] ? nan : ls[e] == 0.f ? 0.f : 1.f / ls[e];
 #pragma unroll
-        for (int i = 0; i < SC_WARPS; ++i) {
-            const float2 v = ml[i * SC_ROWS + r];
-            wt[i] = v.x == SC_NEG_INF ? 0.f : ex2(v.x - M);
-            L += v.x == SC_NEG_INF ? v.y : v.y * wt[i];  // (without a reference the sum is 0 or NaN)
-        }
-        const int row = row0 + r;
-        const float norm = L != L ? nan : !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
-        if (row < P.rows || !whole) {
-            const size_t orow = whole ? sc_out_row(P, w.b, head, row) : 0;
-#pragma unroll
-            for (int i = 0; i < D / (4 * PER); ++i) {
-                const int d = (i * PER + cpart) * 4;
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < SC_WARPS; ++k) {
-                    const float4 v = *reinterpret_cast<const float4*>(all + k * (Sm::MERGE / 4) + r * Sm::MERGE_ROW + d);
-                    a.x = fmaf(wt[k], v.x, a.x);
-                    a.y = fmaf(wt[k], v.y, a.y);
-                    a.z = fmaf(wt[k], v.z, a.z);
-                    a.w = fmaf(wt[k], v.w, a.w);
+                    for (int u8 = 0; u8 < NV; ++u8) {
+                        const float2 y = value(e, u8);
+                        *reinterpret_cast<uint32_t*>(stage + (r8 + 8 * e) * Sm::STAGE_ROW + u8 * 8 + 2 * q4) =
+                            Ty::pack(y.x * norm, y.y * norm);
+                    }
+                    const int row = row0 + r8 + 8 * e;
+                    if (q4 == 0 && P.out_lse && row < P.rows)
+                        P.out_lse[sc_out_row(P, w.b, head, row)] =
+                            ls[e] == 0.f ? SC_NEG_INF : (m[e] + log2f(ls[e])) * SC_LN2;
                 }
-                a.x *= norm, a.y *= norm, a.z *= norm, a.w *= norm;
-                if (whole) {
-                    const uint2 y = make_uint2(Ty::pack(a.x, a.y), Ty::pack(a.z, a.w));
-                    *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + orow * D + d) = y;
-                } else {
-                    *reinterpret_cast<float4*>(P.part_o + (static_cast<size_t>(slot) * SC_ROWS + r) * D + d) = a;
+                __syncwarp();
+#pragma unroll 1
+                for (int i = lane; i < SC_ROWS * (D / 8); i += 32) {
+                    const int r = i / (D / 8), dc = i % (D / 8);
+                    if (row0 + r < P.rows)
+                        *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + sc_out_row(P, w.b, head, row0 + r) * D + dc * 8) =
+                            *reinterpret_cast<const uint4*>(stage + r * Sm::STAGE_ROW + dc * 8);
                 }
+                __syncwarp();
+            } else {
+                const size_t slot = static_cast<size_t>(number) * 2 + (w.u0 == 0 ? 1 : 0);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const size_t at = slot * SC_ROWS + r8 + 8 * e;
+                    if (q4 == 0) P.part_ml[at] = make_float2(m[e], ls[e]);
+#pragma unroll
+                    for (int u8 = 0; u8 < NV; ++u8)
+                        *reinterpret_cast<float2*>(P.part_o + at * D + u8 * 8 + 2 * q4) = value(e, u8);
+                }
+                if (lane == 0 && w.u0 == 0)
+                    P.desc[number] = make_int4(w.b, w.hr, w.parts(static_cast<int>(R.chunk)), 0);
             }
-            if (cpart == 0) {
-                if (!whole)
-                    P.part_ml[static_cast<size_t>(slot) * SC_ROWS + r] = make_float2(M, L);
-                else if (P.out_lse)
-                    P.out_lse[orow] = L == 0.f ? SC_NEG_INF : (M + log2f(L)) * SC_LN2;
+        } else {
+            // ---- merge the warps: 16 rows of (reference, sum, output) each ----
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r8 + 8 * e;
+                if (q4 == 0) ml[warp * SC_ROWS + r] = make_float2(m[e], ls[e]);
+#pragma unroll
+                for (int u8 = 0; u8 < NV; ++u8)
+                    *reinterpret_cast<float2*>(merge + r * Sm::MERGE_ROW + u8 * 8 + 2 * q4) = value(e, u8);
+            }
+            __syncthreads();
+            const float* all = reinterpret_cast<const float*>(sc_raw + Sm::RING);
+            constexpr int PER = SC_NT / SC_ROWS;  // threads of a row
+            const int r = tid / PER, cpart = tid % PER;
+            float M = SC_NEG_INF, L = 0.f, wt[SC_WARPS];
+#pragma unroll
+            for (int i = 0; i < SC_WARPS; ++i) M = fmaxf(M, ml[i * SC_ROWS + r].x);
+#pragma unroll
+            for (int i = 0; i < SC_WARPS; ++i) {
+                const float2 v = ml[i * SC_ROWS + r];
+                wt[i] = v.x == SC_NEG_INF ? 0.f : ex2(v.x - M);
+                L += v.x == SC_NEG_INF ? v.y : v.y * wt[i];  // (without a reference the sum is 0 or NaN)
+            }
+            const int row = row0 + r;
+            const float norm = L != L ? nan : L == 0.f ? 0.f : 1.f / L;
+            if (row < P.rows) {
+                const size_t orow = sc_out_row(P, w.b, head, row);
+#pragma unroll
+                for (int i = 0; i < D / (4 * PER); ++i) {
+                    const int d = (i * PER + cpart) * 4;
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < SC_WARPS; ++k) {
+                        const float4 v =
+                            *reinterpret_cast<const float4*>(all + k * (Sm::MERGE / 4) + r * Sm::MERGE_ROW + d);
+                        a.x = fmaf(wt[k], v.x, a.x);
+                        a.y = fmaf(wt[k], v.y, a.y);
+                        a.z = fmaf(wt[k], v.z, a.z);
+                        a.w = fmaf(wt[k], v.w, a.w);
+                    }
+                    *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + orow * D + d) =
+                        make_uint2(Ty::pack(a.x * norm, a.y * norm), Ty::pack(a.z * norm, a.w * norm));
+                }
+                if (cpart == 0 && P.out_lse) P.out_lse[orow] = L == 0.f ? SC_NEG_INF : (M + log2f(L)) * SC_LN2;
             }
         }
-        if (tid == 0 && w.u0 == 0 && !whole)
-            P.desc[blockIdx.x] = make_int4(w.b, w.hr, w.parts(static_cast<int>(R.chunk)), 0);
-        __syncthreads();  // the merge buffers are free
     }
-    // no copy may land after the CTA is gone (after an error some are still under way)
+    // no copy may land after the warp is gone (after an error some are still under way)
 #pragma unroll 1
     for (; used < issued; ++used)
         if (!sc_wait(&full[used % STAGES], (used / STAGES) & 1, P.timeout_ns)) error = true;
-    if (error && lane == 0 && !P.whole) P.desc[blockIdx.x].w = 1;
+    if (!WHOLE && error && lane == 0) P.desc[number].w = 1;
 }
 
-// K_join: block (i, j) adds the parts of the segment that is cut in CTA i and
+// K_join: block (i, j) adds the parts of the segment that is cut in warp i and
 // begins there, rows 4 j .. 4 j + 3, a warp each, in the order of the parts.
 constexpr int SC_JOIN_NT = 128;
 
@@ -821,7 +877,7 @@ __global__ void __launch_bounds__(SC_JOIN_NT) sc_join_kernel(const __grid_consta
     constexpr int V = D / 32;  // outputs of a lane
     const int r = blockIdx.y * (SC_JOIN_NT / 32) + warp;
     if (row0 + r < P.rows) {
-        // part p lies in the p-th next group's CTA of the same lane
+        // part p lies in the p-th next group's warp of the same lane
         auto slot = [&](int p) { return (blockIdx.x + p * P.lanes) * 2 + (p == 0 ? 1 : 0); };
         float M = SC_NEG_INF;
         for (int p = lane; p < d.z; p += 32) M = fmaxf(M, P.part_ml[static_cast<size_t>(slot(p)) * SC_ROWS + r].x);
@@ -830,7 +886,7 @@ __global__ void __launch_bounds__(SC_JOIN_NT) sc_join_kernel(const __grid_consta
         float L = 0.f, a[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) a[i] = 0.f;
-#pragma unroll 8
+#pragma unroll 16
         for (int p = 0; p < d.z; ++p) {
             const size_t at = static_cast<size_t>(slot(p)) * SC_ROWS + r;
             const float2 v = P.part_ml[at];

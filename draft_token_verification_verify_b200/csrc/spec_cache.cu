@@ -90,34 +90,38 @@ sv_status_t check_cache(const sv_cache_t* c, sv::CacheView* v, int* dt) {
 
 using AttendFn = void (*)(sv::AttendParams);
 
-AttendFn pick_attend(int dt, int D) {
-    if (D == 64) return dt ? sv::sc_attend_kernel<1, 64> : sv::sc_attend_kernel<0, 64>;
-    return dt ? sv::sc_attend_kernel<1, 128> : sv::sc_attend_kernel<0, 128>;
+struct Kernels {
+    AttendFn attend, join;
+    int smem;
+};
+template <int DT, int D>
+Kernels kernels(bool whole) {
+    if (whole) return {sv::sc_attend_kernel<DT, D, true>, nullptr, sv::AttendSmem<D, true>::BYTES};
+    return {sv::sc_attend_kernel<DT, D, false>, sv::sc_join_kernel<DT, D>, sv::AttendSmem<D, false>::BYTES};
 }
-AttendFn pick_join(int dt, int D) {
-    if (D == 64) return dt ? sv::sc_join_kernel<1, 64> : sv::sc_join_kernel<0, 64>;
-    return dt ? sv::sc_join_kernel<1, 128> : sv::sc_join_kernel<0, 128>;
+Kernels pick_attend(int dt, int D, bool whole) {
+    if (D == 64) return dt ? kernels<1, 64>(whole) : kernels<0, 64>(whole);
+    return dt ? kernels<1, 128>(whole) : kernels<0, 128>(whole);
 }
-int attend_smem(int D) { return D == 64 ? sv::AttendSmem<64>::BYTES : sv::AttendSmem<128>::BYTES; }
 
 struct Plan {
     int lanes = 0, passes = 0, cut = 0, grid = 0;
     size_t off_ml = 0, off_desc = 0, bytes = 0;
 };
 
-// The launch shape: a single wave of sc_ctas(D) CTAs an SM, in groups of one for each row block.
+// The launch shape: a single wave of sc_ctas(D) CTAs an SM, their warps in groups of one for each row block.
 bool make_plan(const DeviceInfo& d, int B, int n, int q_heads, int kv_heads, int D, Plan* p) {
     const long long rows = static_cast<long long>(n) * (q_heads / kv_heads);
     if (rows > (1 << 24)) return false;
     const long long blocks = ceil_div(rows, sv::SC_ROWS);
     p->passes = static_cast<int>(ceil_div(blocks, sv::SC_LANES));
     p->lanes = static_cast<int>(ceil_div(blocks, p->passes));
-    p->cut = sv::sc_ctas(D) * d.sms / p->lanes;
-    p->grid = p->cut * p->lanes;
-    const size_t parts = static_cast<size_t>(p->grid) * 2 * sv::SC_ROWS;
+    p->grid = sv::sc_ctas(D) * d.sms;
+    p->cut = p->grid * sv::SC_WARPS / p->lanes;
+    const size_t warps = static_cast<size_t>(p->cut) * p->lanes, parts = warps * 2 * sv::SC_ROWS;
     p->off_ml = round_up(parts * D * sizeof(float), 256);
     p->off_desc = p->off_ml + round_up(parts * sizeof(float2), 256);
-    p->bytes = p->off_desc + round_up(static_cast<size_t>(p->grid) * sizeof(int4), 256);
+    p->bytes = p->off_desc + round_up(warps * sizeof(int4), 256);
     return p->cut > 0 && static_cast<long long>(B) * kv_heads * p->passes * p->lanes < (1LL << 31);
 }
 
@@ -128,12 +132,12 @@ bool attend_sizes_ok(int B, int n, int q_heads, int kv_heads) {
 sv_status_t set_attrs(int dev) {
     std::call_once(g_attr_once[dev], [dev] {
         cudaError_t e = cudaSuccess;
-        for (int dt = 0; dt < 2; ++dt)
-            for (int D = 64; D <= 128; D += 64) {
-                const cudaError_t x = cudaFuncSetAttribute(reinterpret_cast<const void*>(pick_attend(dt, D)),
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem(D));
-                if (x != cudaSuccess) e = x;
-            }
+        for (int i = 0; i < 8; ++i) {
+            const Kernels k = pick_attend(i & 1, (i & 2) ? 128 : 64, (i & 4) != 0);
+            const cudaError_t x = cudaFuncSetAttribute(reinterpret_cast<const void*>(k.attend),
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+            if (x != cudaSuccess) e = x;
+        }
         if (e != cudaSuccess) cudaGetLastError();
         g_attr_err[dev] = e;
     });
@@ -207,8 +211,8 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     // Short contexts (by the page table's width, the lengths being on the device): a CTA takes a whole
     // segment, and one launch does.  That costs less than the join up to
     // kWholeTokens a segment.
-    P.whole = static_cast<long long>(cache->max_pages) * cache->page_size + (k_new ? n : 0) <= kWholeTokens && !out_status;
-    if (P.whole) plan.grid = static_cast<int>(static_cast<long long>(B) * cache->kv_heads * plan.passes * plan.lanes);
+    const bool whole = static_cast<long long>(cache->max_pages) * cache->page_size + (k_new ? n : 0) <= kWholeTokens && !out_status;
+    if (whole) plan.grid = static_cast<int>(static_cast<long long>(B) * cache->kv_heads * plan.passes * plan.lanes);
     P.out = out;
     P.out_lse = out_lse;
     auto* ws = static_cast<unsigned char*>(workspace);
@@ -219,6 +223,7 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     P.test_hook = (opts && opts->test_extra_tx) ? 1 : 0;
     P.out_status = out_status;
 
+    const Kernels fn = pick_attend(dt, D, whole);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (opts && opts->event_start) {
         const sv_status_t e = launched(cudaEventRecord(static_cast<cudaEvent_t>(opts->event_start), st));
@@ -228,25 +233,25 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), 1, 1);
     cfg.blockDim = dim3(sv::SC_NT, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(attend_smem(D));
+    cfg.dynamicSmemBytes = static_cast<size_t>(fn.smem);
     cfg.stream = st;
-    sv_status_t r = launched(cudaLaunchKernelEx(&cfg, pick_attend(dt, D), P));
+    sv_status_t r = launched(cudaLaunchKernelEx(&cfg, fn.attend, P));
     if (r != SV_OK) return r;
     if (opts && opts->event_stop) {
         r = launched(cudaEventRecord(static_cast<cudaEvent_t>(opts->event_stop), st));
         if (r != SV_OK) return r;
     }
-    if (P.whole) return SV_OK;
+    if (whole) return SV_OK;
     cudaLaunchAttribute a[1];
     a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     a[0].val.programmaticStreamSerializationAllowed = 1;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), sv::SC_ROWS / (sv::SC_JOIN_NT / 32), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.cut * plan.lanes), sv::SC_ROWS / (sv::SC_JOIN_NT / 32), 1);
     cfg.blockDim = dim3(sv::SC_JOIN_NT, 1, 1);
     cfg.stream = st;
     cfg.attrs = a;
     cfg.numAttrs = 1;
-    return launched(cudaLaunchKernelEx(&cfg, pick_join(dt, D), P));
+    return launched(cudaLaunchKernelEx(&cfg, fn.join, P));
 }
 
 sv_status_t spec_cache_append(const sv_cache_t* cache, const void* k, const void* v, long long kv_stride, int B,
