@@ -471,10 +471,10 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                     ulonglong2 y;
                     y.x = f2_mul(f2_pack(Ty::lo(kp.x), Ty::lo(kp.y)), kc2);
                     y.y = f2_mul(f2_pack(Ty::hi(kp.x), Ty::hi(kp.y)), sl2);
-                    par_s[2 * lane] = y;
+                    par_s[4 * (lane & 7) + (lane >> 3)] = y;
                     y.x = DT == 0 ? f2_mul(s2, v_code) : s2;
                     y.y = f2_fma(s2, eight2, f2_pack(Ty::hi(vp.x), Ty::hi(vp.y)));
-                    par_s[2 * lane + 1] = y;
+                    par_s[32 + 4 * (lane & 7) + (lane >> 3)] = y;
                     __syncwarp();
                 }
                 // scores: lane r8 of n-tile t takes token 16 (r8 / 2) + 2 t + r8 % 2, so that
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                 const uint64_t n2[2] = {f2_pack(nref[0], nref[0]), f2_pack(nref[1], nref[1])};
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
-                    const ulonglong2 y = par_s[2 * (8 * q4 + t)];
+                    const ulonglong2 y = par_s[4 * t + q4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float* d = &x[t][2 * e];
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                 uint32_t pa[4][4], pl[4][4];
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
-                    const ulonglong2 y = par_s[2 * (8 * q4 + t) + 1];
+                    const ulonglong2 y = par_s[32 + 4 * t + q4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint64_t p2 = f2_pack(ex2(x[t][2 * e]), ex2(x[t][2 * e + 1]));
@@ -578,12 +578,12 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                             sc_mma<0>(o[u4 + i], pa[k], vb[0], vb[1]);
                             if constexpr (DT == 1) sc_mma<0>(o[u4 + i], pl[k], vb[0], vb[1]);
                         }
-                }
-                // bf16 codes count from 0 in the product: 8 of the rounded weights are summed beside
-                // it, so that a weight's rounding meets code - 8 in the end and not code
-                if constexpr (DT == 0) {
+                    // bf16 codes count from 0 in the product: 8 of the rounded weights are summed beside
+                    // it, so that a weight's rounding meets code - 8 in the end and not code
+                    if constexpr (DT == 0) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc_mma<0>(o8, pa[k], 0x00080008u, 0x00800080u);
+                        for (int k = u4 * 4 / NV; k < (u4 + 4) * 4 / NV; ++k) sc_mma<0>(o8, pa[k], 0x00080008u, 0x00800080u);
+                    }
                 }
                 __syncwarp();
                 issue();  // into the stage just read
@@ -602,48 +602,58 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                 }
 #pragma unroll 1
                 for (int j0 = ub; j0 < ub + SC_BLOCK && j0 < P.n; j0 += 16) {
-                    float x[2][4];
+                    // all loads of the 16 positions first: values (zeros behind the last), keys
                     const long long tok = static_cast<long long>(w.b) * P.n;
+                    constexpr int VL = 16 * (D / 8) / 32;
+                    uint4 vx[VL], kx[2][KS / 2];
+#pragma unroll
+                    for (int i = 0; i < VL; ++i) {
+                        const int j = j0 + (i * 32 + lane) / (D / 8), dc = lane % (D / 8);
+                        vx[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (j < P.n)
+                            vx[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.v_new) + (tok + j) * P.kv_stride +
+                                                                    static_cast<long long>(head) * D + dc * 8);
+                    }
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const int j = j0 + 8 * t + r8;
-                        const bool in = j < P.n;
                         const T* src = static_cast<const T*>(P.k_new) + (tok + j) * P.kv_stride +
                                        static_cast<long long>(head) * D + q4 * (D / 4);
+#pragma unroll
+                        for (int i = 0; i < KS / 2; ++i)
+                            kx[t][i] = j < P.n ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    float x[2][4];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) x[t][i] = 0.f;
 #pragma unroll
                         for (int i = 0; i < KS / 2; ++i) {
-                            uint4 kx = in ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                            uint4 y = kx[t][i];
                             if constexpr (DT == 0) {  // against the queries' 2^60
-                                kx.y = Ty::pack(Ty::lo(kx.y) * 16.f, Ty::hi(kx.y) * 16.f);
-                                kx.w = Ty::pack(Ty::lo(kx.w) * 16.f, Ty::hi(kx.w) * 16.f);
+                                y.y = Ty::pack(Ty::lo(y.y) * 16.f, Ty::hi(y.y) * 16.f);
+                                y.w = Ty::pack(Ty::lo(y.w) * 16.f, Ty::hi(y.w) * 16.f);
                             }
-                            sc_mma<DT>(x[t], qa[2 * i], kx.x, kx.y);
-                            sc_mma<DT>(x[t], qa[2 * i + 1], kx.z, kx.w);
+                            sc_mma<DT>(x[t], qa[2 * i], y.x, y.y);
+                            sc_mma<DT>(x[t], qa[2 * i + 1], y.z, y.w);
                         }
                     }
-                    // value rows of the 16 positions, zeros behind the last; a row that is not
-                    // finite is left out of the MMAs, where it would reach the rows that do not
-                    // see it, and added by itself
+                    // the value rows to shared memory; a row that is not finite is left out of the MMAs,
+                    // where it would reach the rows that do not see it, and added by itself
                     T* vs = reinterpret_cast<T*>(merge);
                     uint32_t odd = 0;
                     __syncwarp();
-#pragma unroll 1
-                    for (int i = lane; i < 16 * (D / 8); i += 32) {
-                        const int jr = i / (D / 8), dc = i % (D / 8);
-                        uint4 vx = make_uint4(0u, 0u, 0u, 0u);
-                        if (j0 + jr < P.n)
-                            vx = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.v_new) +
-                                                                 (tok + j0 + jr) * P.kv_stride +
-                                                                 static_cast<long long>(head) * D + dc * 8);
-                        const uint32_t vv[4] = {vx.x, vx.y, vx.z, vx.w};
+#pragma unroll
+                    for (int i = 0; i < VL; ++i) {
+                        const int jr = (i * 32 + lane) / (D / 8), dc = lane % (D / 8);
+                        const uint32_t vv[4] = {vx[i].x, vx[i].y, vx[i].z, vx[i].w};
                         bool fine = true;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             fine &= fabsf(Ty::lo(vv[k])) < __builtin_huge_valf() && fabsf(Ty::hi(vv[k])) < __builtin_huge_valf();
                         if (!fine) odd |= 1u << jr;
-                        *reinterpret_cast<uint4*>(vs + jr * (D + 8) + dc * 8) = vx;
+                        *reinterpret_cast<uint4*>(vs + jr * (D + 8) + dc * 8) = vx[i];
                     }
                     odd = __reduce_or_sync(ALL, odd);
                     if (odd) {
