@@ -34,7 +34,7 @@ constexpr int SC_WARPS = 4;
 constexpr int SC_NT = SC_WARPS * 32;
 constexpr int SC_ROWS = 16;   // rows of a block
 constexpr int SC_LANES = 32;  // row blocks side by side at most
-constexpr int SC_MIN_TILES = 4;  // tiles of a CTA's range at least
+constexpr int SC_MIN_TILES = 2;  // units of a range at least (4: 3 us more where there are few)
 
 // CTAs an SM.  The products of 64 dims fit 168 registers a thread, and a third
 // CTA hides more of a tile's latency than it costs: 128 sequences of 6,200 to

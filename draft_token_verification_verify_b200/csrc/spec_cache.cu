@@ -16,7 +16,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
 constexpr int kMaxPage = 1024;
-constexpr long long kWholeTokens = 1024;  // contexts up to this are not cut
+constexpr long long kWholeTokens = 1024;  // contexts up to this are not cut ...
+constexpr long long kWholeWaves = 3;      // ... where a CTA for each segment makes at most so many waves
 
 struct DeviceInfo {
     bool ok = false;
@@ -208,11 +209,14 @@ sv_status_t spec_cache_attend(const void* q, long long q_stride, const void* k_n
     P.passes = plan.passes;
     P.cut = plan.cut;
     P.scale = scale;
-    // Short contexts (by the page table's width, the lengths being on the device): a CTA takes a whole
-    // segment, and one launch does.  That costs less than the join up to
-    // kWholeTokens a segment.
-    const bool whole = static_cast<long long>(cache->max_pages) * cache->page_size + (k_new ? n : 0) <= kWholeTokens && !out_status;
-    if (whole) plan.grid = static_cast<int>(static_cast<long long>(B) * cache->kv_heads * plan.passes * plan.lanes);
+    // Few segments of short contexts (by the page table's width, the lengths being on the device): a CTA
+    // takes a whole segment, and one launch does.  At 32 query and 8 key heads of 128, 5 positions and 900
+    // tokens that takes 10, 14, 48 and 169 us for 1, 16, 64 and 256 sequences (16, 256, 1024 and 4096
+    // segments), ranges for the warps and a join 14, 20, 45 and 144 us.
+    const long long segments = static_cast<long long>(B) * cache->kv_heads * plan.passes * plan.lanes;
+    const bool whole = static_cast<long long>(cache->max_pages) * cache->page_size + (k_new ? n : 0) <= kWholeTokens &&
+                       segments <= kWholeWaves * plan.grid && !out_status;
+    if (whole) plan.grid = static_cast<int>(segments);
     P.out = out;
     P.out_lse = out_lse;
     auto* ws = static_cast<unsigned char*>(workspace);
