@@ -271,7 +271,10 @@ sv_status_t spec_cache_append(const sv_cache_t* cache, const void* k, const void
         !aligned(out_lens, 4) || (nodes && nodes_stride < n - 1))
         return SV_ERR_INVALID_ARG;
     const bool in_place = out_lens == cache->lens;
-    if (!in_place && out_lens < cache->lens + B && cache->lens < out_lens + B) return SV_ERR_INVALID_ARG;
+    auto overlaps = [&](const int32_t* p, size_t count) { return p && out_lens < p + count && p < out_lens + B; };
+    if ((!in_place && overlaps(cache->lens, B)) || overlaps(n_accepted, B) ||
+        overlaps(nodes, static_cast<size_t>(B) * nodes_stride))
+        return SV_ERR_INVALID_ARG;
     int dev = 0;
     if (!device_info(&dev)) return SV_ERR_UNSUPPORTED;
     sv::AppendParams P;

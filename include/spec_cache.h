@@ -133,7 +133,7 @@ SV_API size_t spec_cache_attend_workspace_size(int B, int n, int q_heads, int kv
  *               node nodes[b][i-1] (the out_nodes of spec_verify_tree, whose
  *               stride is N + 1); NULL: row i is node i
  *   out_lens    [B] int32: the new lengths.  May be cache->lens itself, but
- *               must not overlap it otherwise
+ *               must not overlap it otherwise, nor n_accepted or nodes
  * Rows go to the positions lens[b], lens[b] + 1, ...; the page table must
  * already map them, and the pages written must belong to one sequence alone.
  * A negative length stays as it is and nothing is written.  Data errors: more

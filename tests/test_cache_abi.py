@@ -117,6 +117,17 @@ def test_refusals(L):
     assert sv.spec_cache_attend_workspace_size(2, 3, 4, 2, 128) == 0  # no device
 
 
+def test_append_refuses_lengths_over_its_inputs(L):
+    """New lengths written over the counts or nodes that other CTAs still read."""
+    _no_gpu()
+    c = _cache()
+    for over in (dict(acc=P), dict(acc=P + 4), dict(acc=P - 4), dict(nodes=P, ns=3), dict(nodes=P - 20, ns=3),
+                 dict(acc=1 << 12, out=1 << 12)):
+        assert append(c, **over) == sv.SV_ERR_INVALID_ARG, over
+    for over in (dict(acc=P + 8), dict(acc=P - 8), dict(nodes=P - 24, ns=3), dict(nodes=P + 8, ns=3)):
+        assert append(c, **over) == sv.SV_ERR_UNSUPPORTED, over  # side by side: the arguments are fine
+
+
 def test_kv_cache_refusals():
     ok = torch.zeros((3, 2, 64 * 136), dtype=torch.uint8)
     c = sv.KvCache(ok, 128)

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import draft_token_verification_verify_b200 as sv
-from cachelib import TYPES, Pages, attention, paths
+from cachelib import TYPES, Pages, attention, paths, quantise
 
 pytestmark = pytest.mark.gpu
 
@@ -160,6 +160,101 @@ def test_attend_many_sequences():
     c = Case(lens, 16, 2, 64, torch.bfloat16, 2, seed=11)
     q, k, v = c.tokens(4), c.tokens(2), c.tokens(2)
     check(*c.attend(q, k, v), c.want(q, k, v))
+
+
+@pytest.mark.parametrize("D,cap", [(64, 0), (64, 1100), (128, 0)])
+def test_attend_more_sequences_than_threads(D, cap):
+    """Short contexts of so many sequences that the warps take ranges of them, whole segments among them; two
+    sequences a thread in the search for a range's first.  Some have no tokens or are no sequences."""
+    lens = [(b * 37) % 150 if b % 11 else -(b % 2) for b in range(300)]
+    c = Case(lens, 16, 5, D, torch.bfloat16, 3, seed=37)
+    if cap:
+        c.d_table = torch.cat((c.d_table, torch.zeros((300, cap // 16), dtype=torch.int32, device="cuda:0")), 1)
+    q, k, v = c.tokens(10), c.tokens(5), c.tokens(5)
+    check(*c.attend(q, k, v), c.want(q, k, v))
+    check(*c.attend(q), c.want(q))
+
+
+@pytest.mark.parametrize("n,group,D,lens", [(65, 16, 64, [1100, 40]), (129, 5, 128, [1300]), (33, 33, 128, [20, 2000])])
+def test_attend_more_rows_than_one_pass(n, group, D, lens):
+    """More row blocks than go side by side, the last of them not full; contexts that are cut."""
+    c = Case(lens, 64, 2, D, torch.bfloat16, n, seed=41)
+    q, k, v = c.tokens(2 * group, 1.5), c.tokens(2), c.tokens(2)
+    check(*c.attend(q, k, v), c.want(q, k, v))
+    par = torch.tensor(np.tile(TREES["binary"](n), (len(lens), 1)), dtype=torch.int32)
+    check(*c.attend(q, k, v, par), c.want(q, k, v, par))
+
+
+def test_cut_and_whole_segments_agree():
+    """The form for few short contexts against the one that cuts them: the same attention."""
+    for D in (64, 128):
+        c = Case([700, 3, 0, 450], 64, 2, D, torch.bfloat16, 5, seed=43)
+        q, k, v = c.tokens(8, 1.5), c.tokens(2), c.tokens(2)
+        want = c.want(q, k, v)
+        st = torch.full((1,), 5, dtype=torch.int32, device="cuda:0")
+        check(*c.attend(q, k, v), want)
+        check(*c.attend(q, k, v, out_status=st), want)
+        assert st.item() == sv.SV_OK
+
+
+def test_pages_past_4_gib():
+    """Pages whose offset passes 32 bits: appended to, read and attended as the same pages of a small cache."""
+    c = Case([130], 64, 8, 128, torch.bfloat16, 4, seed=47)
+    q, k, v = c.tokens(32), c.tokens(8), c.tokens(8)
+    num = 64000  # of 69,632 bytes
+    far = torch.empty((num, *c.raw.shape[1:]), dtype=torch.uint8, device="cuda:0")
+    at = torch.tensor([num - 1 - 7 * i for i in range(c.raw.shape[0])], device="cuda:0")
+    far[at] = c.raw
+    big, table = sv.KvCache(far, 128), at[c.d_table.long()].int()
+    outs = []
+    for cache, t in ((c.cache, c.d_table), (big, table)):
+        o = sv.cache_attend(dev(q), cache, t, c.d_lens, dev(k), dev(v))
+        lens = sv.cache_append(cache, t, c.d_lens, dev(k), dev(v))
+        outs.append((o, lens) + sv.cache_read(cache, t, lens, 134))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert torch.equal(far[at], c.raw)
+
+
+def test_two_graphs_replayed_side_by_side():
+    """A step of attention, append and read captured twice, each with its own workspace, on two streams."""
+    steps = []
+    for i in range(2):
+        c = Case([1500, 40 + i, 0], 64, 2, 128, torch.bfloat16, 3, seed=51 + i)
+        q, k, v = c.tokens(8), c.tokens(2), c.tokens(2)
+        want = c.want(q, k, v)
+        d = [dev(x) for x in (q, k, v)]
+        ws = torch.empty(c.cache.workspace_bytes(3, 3, 8), dtype=torch.uint8, device="cuda:0")
+        out, new = torch.empty_like(d[0]), torch.empty(3, dtype=torch.int32, device="cuda:0")
+        rk, rv = (torch.empty((3, 3, 2, 128), dtype=torch.bfloat16, device="cuda:0") for _ in range(2))
+
+        def step(c=c, d=d, ws=ws, out=out, new=new, rk=rk, rv=rv):
+            sv.cache_attend(d[0], c.cache, c.d_table, c.d_lens, d[1], d[2], out=out, workspace=ws)
+            sv.cache_append(c.cache, c.d_table, c.d_lens, d[1], d[2], out_lens=new)
+            sv.cache_read(c.cache, c.d_table, new, 3, first=c.d_lens, out_k=rk, out_v=rv)
+
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        # (with the step, which holds the inputs and the workspace that the graph goes on using)
+        steps.append((c, g, k, v, want, out, new, rk, rv, step, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in steps:
+            s[5].zero_()
+        torch.cuda.synchronize()
+        for s in steps:
+            with torch.cuda.stream(s[-1]):
+                s[1].replay()
+    torch.cuda.synchronize()
+    for c, _, k, v, want, out, new, rk, rv, _, _ in steps:
+        assert bool(((out.cpu().double() - want[0]).abs() <= want[2]).all())
+        assert new.tolist() == [x + 3 for x in c.lens]
+        for x, got in ((k, rk), (v, rv)):
+            codes, scale, zero = quantise(x)
+            assert torch.equal(got.cpu(), (zero.double()[..., None] + scale.double()[..., None] * codes.double()).to(c.T))
 
 
 def test_attend_scale_and_large_scores():
