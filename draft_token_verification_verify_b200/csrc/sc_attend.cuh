@@ -9,9 +9,7 @@
 // so that a weight's rounding meets code - 8.
 //
 // K_attend: a warp takes 16 rows (m16n8k16 MMAs) and tiles of 64 tokens, with a
-// ring of bulk copies of its own, and nothing makes it wait for another: a
-// barrier at each segment's end, where four warps of a CTA took its tiles in
-// turn, cost a third of the time at 24 tiles a segment.  The fragment order
+// ring of bulk copies of its own, and waits for no other warp.  The fragment order
 // is chosen so that a lane's operands are contiguous in the block: 16 (8) bytes
 // of a key row hold the lane's share of the whole dot product, 8 bytes of a
 // value row its 16 tokens.  The reference maximum of a row is not moved until a
@@ -23,7 +21,30 @@
 // the segments' units in a row are cut into equal ranges, one for each group of
 // a single wave, so that a group's warps walk the same tiles side by side and
 // all but the first find them in L2.  A segment that is cut leaves partial sums
-// that K_join adds in the order of the parts.
+// that K_join adds in the order of the parts.  (Four warps of a CTA on the tiles
+// of one segment in turn, merged at its end, took 766 us in place of 618 for 256
+// sequences of up to 3,001 tokens, 72 rows a head: the warps that had fewer
+// tiles waited.)  Where the segments are few and short a CTA does take one
+// whole, its warps the tiles in turn, and there is no K_join.
+//
+// What bounds it: with few rows the bytes of the cache should, but a warp's way
+// through a tile does.  Of its 4,000 clocks the two products take 1,150 each
+// (512 alone: two warps share a scheduler's tensor pipe, which is busy 46 % of
+// the time), maximum and weights 750, wait, parameters and the next copy 700.
+// More warps would hide more of it, but the products of 128 dims need their 241
+// registers: at 168 for a third warp they spill (285 -> 333 us below); half the
+// dims for each of a pair of warps costs more exchanges than it hides (317 ->
+// 377 us); a warp that issues the others' copies takes their registers (283 ->
+// 315 us); 32 rows a warp need the scores in two halves (batched 206 -> 287 us).
+// tcgen05 MMAs, which want 128 rows or codes expanded into tensor memory first,
+// took 533 us in place of 428 at the time.
+// Measured (bf16, 128 dims, 32 query and 8 key heads where not said otherwise):
+//   128 sequences of 6,200-9,800 tokens, 4 positions  272-285 us, 4.0-4.1 TB/s
+//   64 sequences of 500-8,000 tokens, 5 positions     151 us
+//   1 sequence of 131,001 tokens, 9 positions         113 us
+//   256 sequences of 0-3,001, 64 and 8 heads, 9       535 us, 213 TFLOP/s
+//   64 binary trees of 9 nodes on 100-2,300 tokens,
+//     16 and 16 heads of 64, fp16                     59 us
 #pragma once
 
 #include "sc_common.cuh"
@@ -772,32 +793,21 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
             return make_float2(fmaf(o[u][2 * e] - o8[2 * e], os, zs[e]), fmaf(o[u][2 * e + 1] - o8[2 * e], os, zs[e]));
         };
         if constexpr (!WHOLE) {
-            if (w.whole()) {  // through shared memory, to write rows
-                T* stage = reinterpret_cast<T*>(merge);
-                __syncwarp();
+            if (w.whole()) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const int row = row0 + r8 + 8 * e;
+                    if (row >= P.rows) continue;
                     const float norm = ls[e] != ls[e] ? nan : ls[e] == 0.f ? 0.f : 1.f / ls[e];
+                    const size_t orow = sc_out_row(P, w.b, head, row);
 #pragma unroll
                     for (int u8 = 0; u8 < NV; ++u8) {
                         const float2 y = value(e, u8);
-                        *reinterpret_cast<uint32_t*>(stage + (r8 + 8 * e) * Sm::STAGE_ROW + u8 * 8 + 2 * q4) =
+                        *reinterpret_cast<uint32_t*>(static_cast<T*>(P.out) + orow * D + u8 * 8 + 2 * q4) =
                             Ty::pack(y.x * norm, y.y * norm);
                     }
-                    const int row = row0 + r8 + 8 * e;
-                    if (q4 == 0 && P.out_lse && row < P.rows)
-                        P.out_lse[sc_out_row(P, w.b, head, row)] =
-                            ls[e] == 0.f ? SC_NEG_INF : (m[e] + log2f(ls[e])) * SC_LN2;
+                    if (q4 == 0 && P.out_lse) P.out_lse[orow] = ls[e] == 0.f ? SC_NEG_INF : (m[e] + log2f(ls[e])) * SC_LN2;
                 }
-                __syncwarp();
-#pragma unroll 1
-                for (int i = lane; i < SC_ROWS * (D / 8); i += 32) {
-                    const int r = i / (D / 8), dc = i % (D / 8);
-                    if (row0 + r < P.rows)
-                        *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + sc_out_row(P, w.b, head, row0 + r) * D + dc * 8) =
-                            *reinterpret_cast<const uint4*>(stage + r * Sm::STAGE_ROW + dc * 8);
-                }
-                __syncwarp();
             } else {
                 const size_t slot = static_cast<size_t>(number) * 2 + (w.u0 == 0 ? 1 : 0);
 #pragma unroll

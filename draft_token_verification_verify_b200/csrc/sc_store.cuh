@@ -6,8 +6,15 @@
 // D = 128, half a warp at D = 64) takes 8 of them and each lane 4 dims, so that
 // the word of 8 tokens of a value row (values are stored dim by dim) is built,
 // or taken apart, within one lane; the words of the 8 groups meet in shared
-// memory, since those of one group lie a whole row apart.  Nothing is read
-// twice.
+// memory, since those of one group lie a whole row apart (written or read from
+// each group 4 bytes at a time they took 167 us in place of 146, and 147 in place
+// of 119).  Nothing is read twice.
+//
+// Measured, 16 prompts of 2,050 to 8,191 tokens, 8 heads of 128, bf16: append 143
+// us, 3.2 TB/s (bound by instruction issue, 73 % of the slots: about 75
+// instructions a row and warp, of which the search for the smallest and largest
+// element takes 13), read 110 us, 5.2 TB/s (writes 476 MB; near the rate of a
+// copy).  Decoding steps are bound by their launches.
 #pragma once
 
 #include <type_traits>
