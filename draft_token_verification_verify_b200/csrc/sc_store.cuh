@@ -10,10 +10,10 @@
 // each group 4 bytes at a time they took 167 us in place of 146, and 147 in place
 // of 119).  Nothing is read twice.
 //
-// Measured, 16 prompts of 2,050 to 8,191 tokens, 8 heads of 128, bf16: append 143
-// us, 3.2 TB/s (bound by instruction issue, 73 % of the slots: about 75
+// Measured, 16 prompts of 2,717 to 8,191 tokens, 8 heads of 128, bf16: append 143
+// us, 466 MB at 3.3 TB/s (bound by instruction issue, 73 % of the slots: about 75
 // instructions a row and warp, of which the search for the smallest and largest
-// element takes 13), read 110 us, 5.2 TB/s (writes 476 MB; near the rate of a
+// element takes 13), read back 110 us, 635 MB at 5.8 TB/s (88 % of the rate of a
 // copy).  Decoding steps are bound by their launches.
 #pragma once
 
