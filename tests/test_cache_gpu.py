@@ -197,6 +197,34 @@ def test_cut_and_whole_segments_agree():
         assert st.item() == sv.SV_OK
 
 
+@pytest.mark.parametrize("lens", [[300, 70], [3000, 70]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_magnitudes(D, lens):
+    """Powers of two on the keys (and their inverse on the queries) and on the values change no rounding: the
+    same bits times the values' power, over the range that is documented."""
+    T = torch.bfloat16
+    first = None
+    for ek, ev in ((0, 0), (-55, 0), (55, 0), (0, -60), (0, 52), (30, -30)):
+        c = Case(lens, 64, 2, D, T, 3, seed=59)
+        for part, e in ((0, ek), (1, ev)):
+            c.pages.params[part] = (c.pages.params[part].double() * 2.0 ** e).to(T)
+        c.raw.copy_(c.pages.bytes())
+        q, k, v = (x.double() for x in (c.tokens(8, 1.5), c.tokens(2), c.tokens(2)))
+        out, lse = c.attend((q * 2.0 ** -ek).to(T), (k * 2.0 ** ek).to(T), (v * 2.0 ** ev).to(T))
+        if first is None:
+            first = out, lse
+        assert torch.equal(lse, first[1]), (ek, ev)
+        if ev > -50:
+            assert torch.equal(out, first[0] * 2.0 ** ev), (ek, ev)
+        else:
+            # a weight of a long context times 2^-60 and a code's 2^-133 lies among fp32's subnormals: each of at
+            # most as many additions as tokens is off by half their spacing, 2^-150, which the output's 2^69
+            # makes 2^-81 (the sum of weights it is divided by is at least 1), for the sum and the one of 8 each;
+            # where that crosses a rounding to bf16, one step, 2^-7 of the output, more
+            off = (out - first[0] * 2.0 ** ev).abs()
+            assert bool((off <= 2.0 ** -7 * out.abs() + 2 * (max(lens) + 3) * 2.0 ** -81).all()), (ek, ev)
+
+
 def test_pages_past_4_gib():
     """Pages whose offset passes 32 bits: appended to, read and attended as the same pages of a small cache."""
     c = Case([130], 64, 8, 128, torch.bfloat16, 4, seed=47)
