@@ -132,6 +132,8 @@ class KvCache:
         code = SV_DTYPE_F16 if dtype == torch.float16 else 0
         self._struct = SvCache(pages.data_ptr(), None, None, self.num_pages, 0, size, self.kv_heads, self.head_dim, code)
         self._index = pages.get_device()
+        self._torch = torch  # (an import in each check costs a good part of it)
+        self._like = pages.new_empty(0, dtype=dtype)
         self._workspace = {}  # bytes by (B, n, q_heads)
 
     @classmethod
@@ -162,8 +164,7 @@ class KvCache:
 
 def _ints(t, name, shape, cache):
     """Checks a contiguous int32 tensor of `shape` on the pages' device."""
-    import torch
-
+    torch = cache._torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not torch.int32:
@@ -180,9 +181,7 @@ def _tokens(t, name, cache, heads=None):
     """Checks activations [B, n, heads, D] whose heads lie side by side and
     whose tokens are evenly spaced (a part of a fused projection's rows will
     do); returns (shape, elements between tokens)."""
-    import torch
-
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, cache._torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not cache.dtype:
         raise TypeError(f"{name} must be {cache.dtype} like the cache, got {t.dtype}")
@@ -192,10 +191,12 @@ def _tokens(t, name, cache, heads=None):
     if t.get_device() != cache._index:
         raise ValueError(f"{name} is on {t.device}, the pages on {cache.device}")
     B, n, H, D = shape
-    sb, sn, sh, sd = t.stride()
-    step = sn if n > 1 else sb if B > 1 else H * D
-    if sd != 1 or (H > 1 and sh != D) or (n > 1 and B > 1 and sb != n * sn) or step < H * D:
-        raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, got strides {t.stride()}")
+    step = H * D
+    if not t.is_contiguous():
+        sb, sn, sh, sd = t.stride()
+        step = sn if n > 1 else sb if B > 1 else step
+        if sd != 1 or (H > 1 and sh != D) or (n > 1 and B > 1 and sb != n * sn) or step < H * D:
+            raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, got strides {t.stride()}")
     if step % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name}: tokens must be 16-byte aligned")
     return shape, step
@@ -208,14 +209,12 @@ def _out(t, name, dtype, shape, cache):
 
 def _batch(cache, page_table, lens, B):
     """Checks the page table and lengths of B sequences."""
-    import torch
-
     if not isinstance(cache, KvCache):
         raise TypeError("cache must be a KvCache")
     if cache._index < 0:
         raise ValueError(f"tensors must be on a CUDA device, got {cache.device}")
     _ints(lens, "lens", (B,), cache)
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[1] < 1:
+    if not isinstance(page_table, cache._torch.Tensor) or page_table.dim() != 2 or page_table.shape[1] < 1:
         raise ValueError("page_table must be a [B, max_pages] tensor")
     _ints(page_table, "page_table", (B, page_table.shape[1]), cache)
 
@@ -223,8 +222,7 @@ def _batch(cache, page_table, lens, B):
 def _on(cache, stream, call):
     """Runs ``call(raw stream)`` with the pages' device current and what it
     allocates belonging to the stream it runs on."""
-    import torch
-
+    torch = cache._torch
     # (torch.cuda's own functions of these names cost several times the launch)
     if torch._C._cuda_getDevice() != cache._index:
         with torch.cuda.device(cache._index):
@@ -248,8 +246,6 @@ def cache_attend(q, cache: KvCache, page_table, lens, k=None, v=None, parents=No
     int32.  Optional: out [B, n, q_heads, D], out_lse [B, n, q_heads] fp32,
     out_status [1] int32, workspace (uint8, allocated with torch when None; calls
     that can overlap need one each).  Returns out."""
-    import torch
-
     if not isinstance(cache, KvCache):
         raise TypeError("cache must be a KvCache")
     (B, n, Hq, D), q_step = _tokens(q, "q", cache)
@@ -276,14 +272,16 @@ def cache_attend(q, cache: KvCache, page_table, lens, k=None, v=None, parents=No
     if out is not None:
         _out(out, "out", cache.dtype, q.shape, cache)
     if out_lse is not None:
-        _out(out_lse, "out_lse", torch.float32, (B, n, Hq), cache)
+        _out(out_lse, "out_lse", cache._torch.float32, (B, n, Hq), cache)
     if out_status is not None:
         _ints(out_status, "out_status", (1,), cache)
     if workspace is not None and (workspace.get_device() != cache._index or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be contiguous on {dev}")
 
     def call(raw):
-        o = q.new_empty((B, n, Hq, D)) if out is None else out
+        o = out
+        if o is None:
+            o = cache._torch.empty_like(q) if q.is_contiguous() else q.new_empty((B, n, Hq, D))
         ws = cache.pages.new_empty(cache.workspace_bytes(B, n, Hq)) if workspace is None else workspace
         st = cache_lib().spec_cache_attend(
             q.data_ptr(), q_step, k_ptr, v_ptr, kv_step, None if parents is None or n == 1 else parents.data_ptr(),
@@ -305,8 +303,6 @@ def cache_append(cache: KvCache, page_table, lens, k, v, n_accepted=None, nodes=
     ``out_nodes`` of ``verify_tree``), None row i.  ``out_lens`` [B] int32 may be
     ``lens`` itself, which is then advanced in place; a new tensor when None.
     Returns the new lengths (-1: a data error of that sequence)."""
-    import torch
-
     if not isinstance(cache, KvCache):
         raise TypeError("cache must be a KvCache")
     shape, step = _tokens(k, "k", cache, cache.kv_heads)
@@ -319,7 +315,7 @@ def cache_append(cache: KvCache, page_table, lens, k, v, n_accepted=None, nodes=
         _ints(n_accepted, "n_accepted", (B,), cache)
     stride = 0
     if nodes is not None:
-        if not isinstance(nodes, torch.Tensor) or nodes.dim() != 2 or nodes.shape[1] < n - 1:
+        if not isinstance(nodes, cache._torch.Tensor) or nodes.dim() != 2 or nodes.shape[1] < n - 1:
             raise ValueError(f"nodes must be [B, >= {n - 1}]")
         stride = nodes.shape[1]
         _ints(nodes, "nodes", (B, stride), cache)
@@ -343,9 +339,9 @@ def cache_read(cache: KvCache, page_table, lens, n: int, first=None, out_k=None,
     """Positions first[b] .. first[b] + n - 1 of every sequence (``first`` [B]
     int32, None: 0) as (k, v), each [B, n, kv_heads, D] in the cache's type;
     rows outside a sequence's ``lens`` tokens are zeros."""
-    import torch
-
-    if not isinstance(lens, torch.Tensor) or lens.dim() != 1:
+    if not isinstance(cache, KvCache):
+        raise TypeError("cache must be a KvCache")
+    if not isinstance(lens, cache._torch.Tensor) or lens.dim() != 1:
         raise ValueError("lens must be a [B] tensor")
     B = lens.shape[0]
     _batch(cache, page_table, lens, B)
@@ -360,8 +356,8 @@ def cache_read(cache: KvCache, page_table, lens, n: int, first=None, out_k=None,
         _out(out_v, "out_v", cache.dtype, shape, cache)
 
     def call(raw):
-        ko = torch.empty(shape, dtype=cache.dtype, device=cache.device) if out_k is None else out_k
-        vo = torch.empty(shape, dtype=cache.dtype, device=cache.device) if out_v is None else out_v
+        ko = cache._like.new_empty(shape) if out_k is None else out_k
+        vo = cache._torch.empty_like(ko) if out_v is None else out_v
         st = cache_lib().spec_cache_read(ctypes.byref(cache.struct(page_table, lens)), B, n,
                                          None if first is None else first.data_ptr(), ko.data_ptr(), vo.data_ptr(), raw)
         if st != 0:
