@@ -29,8 +29,10 @@
 //
 // What bounds it: with few rows the bytes of the cache should, but a warp's way
 // through a tile does.  Of its 4,000 clocks the two products take 1,150 each
-// (512 alone: two warps share a scheduler's tensor pipe, which is busy 46 % of
-// the time), maximum and weights 750, wait, parameters and the next copy 700.
+// (950 with the scheduler's other warp kept out of them: a warp alone issues one
+// of these MMAs and the masks for it every 14 clocks, so taking turns gains
+// nothing; the pipe, at 8 clocks each, is busy 46 % of the time), maximum and
+// weights 750, wait, parameters and the next copy 700.
 // More warps would hide more of it, but the products of 128 dims need their 241
 // registers: at 168 for a third warp they spill (285 -> 333 us below); half the
 // dims for each of a pair of warps costs more exchanges than it hides (317 ->
