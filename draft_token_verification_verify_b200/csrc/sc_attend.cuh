@@ -27,19 +27,22 @@
 // tiles waited.)  Where the segments are few and short a CTA does take one
 // whole, its warps the tiles in turn, and there is no K_join.
 //
-// What bounds it: with few rows the bytes of the cache should, but a warp's way
-// through a tile does.  Of its 4,000 clocks the two products take 1,150 each
-// (950 with the scheduler's other warp kept out of them: a warp alone issues one
-// of these MMAs and the masks for it every 14 clocks, so taking turns gains
-// nothing; the pipe, at 8 clocks each, is busy 46 % of the time), maximum and
-// weights 750, wait, parameters and the next copy 700.
-// More warps would hide more of it, but the products of 128 dims need their 241
+// What bounds it: with few rows the bytes of the cache should, but the MMAs with
+// the masks of their operands do.  The pipe takes an MMA every 9.2 clocks; with
+// its masks (2.5 integer instructions, which do not overlap with it fully) the
+// two warps of a scheduler reach one every 10.5 to 12, so that the 132 of a tile
+// are 2,800 to 3,200 of the 4,000 clocks in which each of the two warps does a
+// tile; the rest of a warp's way through it (maximum and weights 750 clocks,
+// wait, parameters and the next copy 700) is hidden but for that.  The order of
+// the MMAs and masks in the source, 8 accumulators in place of 4, or a lock that
+// gives the warps turns made no difference.
+// More warps would hide the rest, but the products of 128 dims need their 241
 // registers: at 168 for a third warp they spill (285 -> 333 us below); half the
 // dims for each of a pair of warps costs more exchanges than it hides (317 ->
 // 377 us); a warp that issues the others' copies takes their registers (283 ->
-// 315 us); 32 rows a warp need the scores in two halves (batched 206 -> 287 us).
-// tcgen05 MMAs, which want 128 rows or codes expanded into tensor memory first,
-// took 533 us in place of 428 at the time.
+// 315 us).  32 rows a warp share the masks but need the scores in two halves
+// (batched 206 -> 287 us).  tcgen05 MMAs, which want 128 rows or codes expanded
+// into tensor memory first, took 533 us in place of 428 at the time.
 // Measured (bf16, 128 dims, 32 query and 8 key heads where not said otherwise):
 //   128 sequences of 6,200-9,800 tokens, 4 positions  272-285 us, 4.0-4.1 TB/s
 //   64 sequences of 500-8,000 tokens, 5 positions     151 us
@@ -62,8 +65,8 @@ constexpr int SC_MIN_TILES = 2;  // units of a range at least (4: 3 us more wher
 // CTAs an SM.  The products of 64 dims fit 168 registers a thread, and a third
 // CTA hides more of a tile's latency than it costs: 128 sequences of 6,200 to
 // 9,800 tokens, 32 query and 8 key heads, 4 positions, 239 -> 216 us; 64 trees
-// of 9 nodes on up to 2,300 tokens in fp16, 129 -> 106 us.  Those of 128 dims
-// spill there (317 -> 432 us).
+// of 9 nodes on up to 2,300 tokens in fp16, 129 -> 106 us (before the warps had
+// ranges of their own).  Those of 128 dims spill there.
 constexpr int sc_ctas(int D) { return D == 64 ? 3 : 2; }
 
 struct AttendParams {
