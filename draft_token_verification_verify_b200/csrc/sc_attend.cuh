@@ -412,10 +412,10 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                 qs[e] += (Ty::lo(x.x) + Ty::hi(x.x)) + (Ty::lo(x.y) + Ty::hi(x.y)) + (Ty::lo(x.z) + Ty::hi(x.z)) +
                          (Ty::lo(x.w) + Ty::hi(x.w));
                 if constexpr (DT == 0) {  // 2^64, and 2^60 where the code is 16-fold (exact)
-                    x.x = Ty::pack(Ty::lo(x.x) * SC_2P64, Ty::hi(x.x) * SC_2P64);
-                    x.y = Ty::pack(Ty::lo(x.y) * SC_2P60, Ty::hi(x.y) * SC_2P60);
-                    x.z = Ty::pack(Ty::lo(x.z) * SC_2P64, Ty::hi(x.z) * SC_2P64);
-                    x.w = Ty::pack(Ty::lo(x.w) * SC_2P60, Ty::hi(x.w) * SC_2P60);
+                    x.x = sc_times(x.x, 0x5F805F80u);
+                    x.y = sc_times(x.y, 0x5D805D80u);
+                    x.z = sc_times(x.z, 0x5F805F80u);
+                    x.w = sc_times(x.w, 0x5D805D80u);
                 }
                 qa[2 * i][e] = x.x;
                 qa[2 * i][2 + e] = x.y;
@@ -658,8 +658,8 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                         for (int i = 0; i < KS / 2; ++i) {
                             uint4 y = kx[t][i];
                             if constexpr (DT == 0) {  // against the queries' 2^60
-                                y.y = Ty::pack(Ty::lo(y.y) * 16.f, Ty::hi(y.y) * 16.f);
-                                y.w = Ty::pack(Ty::lo(y.w) * 16.f, Ty::hi(y.w) * 16.f);
+                                y.y = sc_times(y.y, 0x41804180u);
+                                y.w = sc_times(y.w, 0x41804180u);
                             }
                             sc_mma<DT>(x[t], qa[2 * i], y.x, y.y);
                             sc_mma<DT>(x[t], qa[2 * i + 1], y.z, y.w);
@@ -673,12 +673,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
 #pragma unroll
                     for (int i = 0; i < VL; ++i) {
                         const int jr = (i * 32 + lane) / (D / 8), dc = lane % (D / 8);
-                        const uint32_t vv[4] = {vx[i].x, vx[i].y, vx[i].z, vx[i].w};
-                        bool fine = true;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            fine &= fabsf(Ty::lo(vv[k])) < __builtin_huge_valf() && fabsf(Ty::hi(vv[k])) < __builtin_huge_valf();
-                        if (!fine) odd |= 1u << jr;
+                        if (!sc_finite<DT>(vx[i])) odd |= 1u << jr;
                         *reinterpret_cast<uint4*>(vs + jr * (D + 8) + dc * 8) = vx[i];
                     }
                     odd = __reduce_or_sync(ALL, odd);

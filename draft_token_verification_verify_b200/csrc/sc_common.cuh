@@ -180,6 +180,20 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Both halves of a bf16 pair times a power of two (given twice): exact but for overflow.
+__device__ __forceinline__ uint32_t sc_times(uint32_t x, uint32_t power) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(power));
+    return d;
+}
+// Whether all 8 numbers are finite.
+template <int DT>
+__device__ __forceinline__ bool sc_finite(const uint4& x) {
+    const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    return ((m + (DT == 0 ? 0x00800080u : 0x04000400u)) & 0x80008000u) == 0u;  // an exponent of ones carries
+}
+
 // m16n8k16 on the tensor cores, fp32 accumulators.
 template <int DT>
 __device__ __forceinline__ void sc_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
