@@ -397,7 +397,6 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
         const int head = w.hr / P.passes, row0 = ((w.hr - head * P.passes) * P.lanes + row_lane) * SC_ROWS;
         // ---- this segment's queries, in fragment order ----
         uint32_t qa[KS][4];
-        float qs[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = row0 + r8 + 8 * e;
@@ -409,8 +408,6 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < KS / 2; ++i) {
                 uint4 x = in ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-                qs[e] += (Ty::lo(x.x) + Ty::hi(x.x)) + (Ty::lo(x.y) + Ty::hi(x.y)) + (Ty::lo(x.z) + Ty::hi(x.z)) +
-                         (Ty::lo(x.w) + Ty::hi(x.w));
                 if constexpr (DT == 0) {  // 2^64, and 2^60 where the code is 16-fold (exact)
                     x.x = sc_times(x.x, 0x5F805F80u);
                     x.y = sc_times(x.y, 0x5D805D80u);
@@ -422,9 +419,13 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                 qa[2 * i + 1][e] = x.z;
                 qa[2 * i + 1][2 + e] = x.w;
             }
-            qs[e] += __shfl_xor_sync(ALL, qs[e], 1);
-            qs[e] += __shfl_xor_sync(ALL, qs[e], 2);
         }
+        // their sums: products with the inverse powers (fp16: with 1), alike in every column
+        float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+            sc_mma<DT>(sums, qa[k], DT == 0 ? 0x1F801F80u : 0x3C003C00u, DT == 0 ? 0x21802180u : 0x3C003C00u);
+        const float qs[2] = {sums[0], sums[2]};
         float o[NV][4], o8[4];  // the output, and 8 of every weight
 #pragma unroll
         for (int u = 0; u < NV; ++u)
