@@ -790,8 +790,12 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
             zs[e] += __shfl_xor_sync(ALL, zs[e], 1);
             zs[e] += __shfl_xor_sync(ALL, zs[e], 2);
         }
-        auto value = [&](int e, int u) {  // dims 8 u + 2 q4, + 1 of the row r8 + 8 e, not yet divided by the sum
-            return make_float2(fmaf(o[u][2 * e] - o8[2 * e], os, zs[e]), fmaf(o[u][2 * e + 1] - o8[2 * e], os, zs[e]));
+        auto value = [&](int e, int u, float by) {  // dims 8 u + 2 q4, + 1 of the row r8 + 8 e, times `by`
+            const float mo = os * by, mz = zs[e] * by;
+            float2 y;
+            f2_unpack(f2_fma(f2_add(f2_pack(o[u][2 * e], o[u][2 * e + 1]), f2_pack(-o8[2 * e], -o8[2 * e])),
+                             f2_pack(mo, mo), f2_pack(mz, mz)), y.x, y.y);
+            return y;
         };
         if constexpr (!WHOLE) {
             if (w.whole()) {
@@ -803,9 +807,8 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                     const size_t orow = sc_out_row(P, w.b, head, row);
 #pragma unroll
                     for (int u8 = 0; u8 < NV; ++u8) {
-                        const float2 y = value(e, u8);
-                        *reinterpret_cast<uint32_t*>(static_cast<T*>(P.out) + orow * D + u8 * 8 + 2 * q4) =
-                            Ty::pack(y.x * norm, y.y * norm);
+                        const float2 y = value(e, u8, norm);
+                        *reinterpret_cast<uint32_t*>(static_cast<T*>(P.out) + orow * D + u8 * 8 + 2 * q4) = Ty::pack(y.x, y.y);
                     }
                     if (q4 == 0 && P.out_lse) P.out_lse[orow] = ls[e] == 0.f ? SC_NEG_INF : (m[e] + log2f(ls[e])) * SC_LN2;
                 }
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                     if (q4 == 0) P.part_ml[at] = make_float2(m[e], ls[e]);
 #pragma unroll
                     for (int u8 = 0; u8 < NV; ++u8)
-                        *reinterpret_cast<float2*>(P.part_o + at * D + u8 * 8 + 2 * q4) = value(e, u8);
+                        *reinterpret_cast<float2*>(P.part_o + at * D + u8 * 8 + 2 * q4) = value(e, u8, 1.f);
                 }
                 if (lane == 0 && w.u0 == 0)
                     P.desc[number] = make_int4(w.b, w.hr, w.parts(static_cast<int>(R.chunk)), 0);
@@ -830,7 +833,7 @@ __global__ void __launch_bounds__(SC_NT, sc_ctas(D)) sc_attend_kernel(const __gr
                 if (q4 == 0) ml[warp * SC_ROWS + r] = make_float2(m[e], ls[e]);
 #pragma unroll
                 for (int u8 = 0; u8 < NV; ++u8)
-                    *reinterpret_cast<float2*>(merge + r * Sm::MERGE_ROW + u8 * 8 + 2 * q4) = value(e, u8);
+                    *reinterpret_cast<float2*>(merge + r * Sm::MERGE_ROW + u8 * 8 + 2 * q4) = value(e, u8, 1.f);
             }
             __syncthreads();
             const float* all = reinterpret_cast<const float*>(sc_raw + Sm::RING);
