@@ -43,11 +43,15 @@
 // 315 us).  32 rows a warp share the masks but need the scores in two halves
 // (batched 206 -> 287 us).  tcgen05 MMAs, which want 128 rows or codes expanded
 // into tensor memory first, took 533 us in place of 428 at the time.
+// Segments of a few tiles are bound by instruction fetches: a tile, the scored
+// positions, queries and outputs together are more code than the SM's
+// instruction cache holds (173 sequences of up to 323 tokens, 17 positions, 48 and
+// 16 heads: 252 -> 179 us from less code between the tiles).
 // Measured (bf16, 128 dims, 32 query and 8 key heads where not said otherwise):
 //   128 sequences of 6,200-9,800 tokens, 4 positions  272-285 us, 4.0-4.1 TB/s
-//   64 sequences of 500-8,000 tokens, 5 positions     151 us
+//   64 sequences of 500-8,000 tokens, 5 positions     148 us
 //   1 sequence of 131,001 tokens, 9 positions         113 us
-//   256 sequences of 0-3,001, 64 and 8 heads, 9       535 us, 213 TFLOP/s
+//   256 sequences of 0-3,001, 64 and 8 heads, 9       516 us, 221 TFLOP/s
 //   64 binary trees of 9 nodes on 100-2,300 tokens,
 //     16 and 16 heads of 64, fp16                     59 us
 #pragma once
