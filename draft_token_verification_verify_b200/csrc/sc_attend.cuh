@@ -36,7 +36,7 @@
 // wait, parameters and the next copy 700) is hidden but for that.  The order of
 // the MMAs and masks in the source, 8 accumulators in place of 4, or a lock that
 // gives the warps turns made no difference.
-// More warps would hide the rest, but the products of 128 dims need their 241
+// More warps would hide the rest, but the products of 128 dims need their 242
 // registers: at 168 for a third warp they spill (285 -> 333 us below); half the
 // dims for each of a pair of warps costs more exchanges than it hides (317 ->
 // 377 us); a warp that issues the others' copies takes their registers (283 ->
@@ -48,7 +48,7 @@
 // instruction cache holds (173 sequences of up to 323 tokens, 17 positions, 48 and
 // 16 heads: 252 -> 179 us from less code between the tiles).
 // Measured (bf16, 128 dims, 32 query and 8 key heads where not said otherwise):
-//   128 sequences of 6,200-9,800 tokens, 4 positions  272-285 us, 4.0-4.1 TB/s
+//   128 sequences of 6,200-9,800 tokens, 4 positions  270-292 us, 3.9-4.2 TB/s
 //   64 sequences of 500-8,000 tokens, 5 positions     148 us
 //   1 sequence of 131,001 tokens, 9 positions         113 us
 //   256 sequences of 0-3,001, 64 and 8 heads, 9       516 us, 221 TFLOP/s
